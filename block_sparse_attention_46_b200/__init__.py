@@ -23,6 +23,8 @@ __all__ = [
     "lf_select_chunk_cached", "lf_cag_schedule", "lf_select_chunk_1d",
     "lf_status_string", "lf_abi_version", "lf_debug_configure", "lf_select_current",
     "lf_quantize_e4m3", "lf_e4m3_head_scales", "lf_block_sparse_attn_e4m3",
+    "lf_attn_backward_workspace_size", "lf_block_sparse_attn_backward", "LfRope", "make_rope",
+    "lf_rope_frames", "lf_rope_backward_workspace_size", "lf_rope_frames_backward",
     "derived", "current_blocks", "LIB_PATH",
 ]
 
@@ -46,11 +48,21 @@ class LfShape(ctypes.Structure):
                 ("k_c", ctypes.c_int32)]
 
 
+class LfRope(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int32), ("d", ctypes.c_int32), ("n_frames", ctypes.c_int32),
+                ("height", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("pairs_t", ctypes.c_int32), ("pairs_h", ctypes.c_int32),
+                ("pairs_w", ctypes.c_int32), ("halves", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("base", ctypes.c_double)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _SHP = ctypes.POINTER(LfShape)
+_RPP = ctypes.POINTER(LfRope)
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
 
 _SIGS = {
     "lf_compress": (ctypes.c_int, [_SHP, _P, _P, _I32P, _P, _P, _P, _P]),
@@ -84,6 +96,14 @@ _SIGS = {
     "lf_pool_frames": (ctypes.c_int, [_SHP, _P, _I32P, ctypes.c_int32, _P, _P]),
     "lf_select_chunk_cached": (ctypes.c_int, [_SHP, _P, _P, _I32P, _P, _P, _SZ, _P]),
     "lf_select_chunk_1d": (ctypes.c_int, [_SHP, _P, _P, _I32P, _P, _P, _SZ, _P]),
+    "lf_attn_backward_workspace_size": (_SZ, [_SHP]),
+    "lf_block_sparse_attn_backward": (ctypes.c_int, [_SHP, _P, _P, _P, _P, _P, _I32P, _I32P] +
+                                      [_P] * 11 + [_SZ, _P]),
+    "lf_rope_frames": (ctypes.c_int, [_RPP, _P, _I64, _I32, _I32P, _I32P, _P, _P, _I32, _I32P,
+                                      _P]),
+    "lf_rope_backward_workspace_size": (_SZ, [_RPP]),
+    "lf_rope_frames_backward": (ctypes.c_int, [_RPP, _P, _I64, _I32, _I32P, _I32P, _P, _P, _I32,
+                                               _I32P, _P, _I64, _P, _P, _SZ, _P]),
     "lf_block_sparse_attn_noalloc": (ctypes.c_int, [_SHP, _P, _P, _P, _P, _P, _I32P, _I32P, _P,
                                                     _P, _P, _P]),
 }
@@ -366,3 +386,166 @@ def lf_forward_chunk(shape, q, k_cur, v_cur, k_cache, v_cache, hist_slots, sink_
         ctypes.byref(sh), _ptr(q), _ptr(k_cur), _ptr(v_cur), _ptr(k_cache), _ptr(v_cache), hs, ss,
         _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse), _ptr(block_idx_out),
         _ptr(cur_idx_out), _stream(stream)), "lf_forward_chunk")
+
+
+# ------------------------------------------------------------------ gradient, rotary positions
+def _on(device, what, dtype, count, **tensors):
+    """Checks what the C side cannot see of the given tensors: one device, type and size."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{what}: {name} is on {t.device}, not {device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{what}: {name} is {t.dtype}, not {dtype}")
+        if count is not None and t.numel() != count:
+            raise ValueError(f"{what}: {name} has {t.numel()} elements, not {count}")
+
+
+def _workspace(workspace, size, device, stream):
+    """The caller's workspace, or one of `size` bytes from the memory of the stream that the
+    call runs on, which may be reused once that stream is past the call."""
+    if workspace is None and size > 0:
+        with torch.cuda.stream(stream):               # None: the current stream
+            workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def lf_attn_backward_workspace_size(shape) -> int:
+    sh = make_shape(shape)
+    return int(load().lf_attn_backward_workspace_size(ctypes.byref(sh)))
+
+
+def lf_block_sparse_attn_backward(shape, q, k_cur, v_cur, k_cache, v_cache, hist_slots,
+                                  sink_slots, block_idx, out, dout, lse, dq, dk_cur, dv_cur,
+                                  dk_cache=None, dv_cache=None, workspace=None, stream=None,
+                                  cur_idx=None):
+    """Gradient of lf_block_sparse_attn (or of the attention of lf_forward_chunk): dq, dk_cur
+    and dv_cur, and with dk_cache and dv_cache the gradient into the listed cache slots, from
+    the forward call's out and lse and the gradient dout of out."""
+    sh = make_shape(shape)
+    what = "lf_block_sparse_attn_backward"
+    dev, bf = q.device, torch.bfloat16
+    if len(hist_slots) != shape.n_hist or len(sink_slots) != shape.n_sink:
+        raise ValueError(f"{what}: slot lists do not match the shape's frames")
+    _, nqb, kf, kb = derived(shape)
+    ncur = shape.n_cur_frames * shape.T
+    cached = shape.n_slots * shape.T * shape.H * shape.d
+    _on(dev, what, bf, ncur * shape.H * shape.d, q=q, k_cur=k_cur, v_cur=v_cur, out=out,
+        dout=dout, dq=dq, dk_cur=dk_cur, dv_cur=dv_cur)
+    _on(dev, what, torch.float32, shape.H * ncur, lse=lse)
+    if shape.n_hist + shape.n_sink > 0:
+        _on(dev, what, bf, cached, k_cache=k_cache, v_cache=v_cache, dk_cache=dk_cache,
+            dv_cache=dv_cache)
+    if shape.n_hist > 0:
+        _on(dev, what, torch.int32, shape.H * nqb * kf * kb, block_idx=block_idx)
+    if current_blocks(shape) > 0:
+        _on(dev, what, torch.int32, shape.H * nqb * current_blocks(shape), cur_idx=cur_idx)
+    hs, _k1 = _slots(hist_slots)
+    ss, _k2 = _slots(sink_slots)
+    with torch.cuda.device(dev):
+        workspace, size = _workspace(workspace, lf_attn_backward_workspace_size(shape), dev, stream)
+        _on(dev, what, torch.uint8, None, workspace=workspace)
+        _check(load().lf_block_sparse_attn_backward(
+            ctypes.byref(sh), _ptr(q), _ptr(k_cur), _ptr(v_cur), _ptr(k_cache), _ptr(v_cache), hs,
+            ss, _ptr(block_idx), _ptr(cur_idx), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq),
+            _ptr(dk_cur), _ptr(dv_cur), _ptr(dk_cache), _ptr(dv_cache), _ptr(workspace), size,
+            _stream(stream)), what)
+
+
+_NORMS = {None: 0, "head": 1, "token": 2, "row": 2}
+
+
+def make_rope(H, d, n_frames, height, width, pairs, halves=False, norm=None, base=10000.0,
+              eps=1e-6) -> LfRope:
+    """lf_rope: heads, head dimension, frames and their token grid, channel pairs per axis
+    (time, height, width), pairing, norm (None, "head" or "row", over the whole token)."""
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {list(_NORMS)}")
+    return LfRope(H, d, n_frames, height, width, *[int(p) for p in pairs], 1 if halves else 0,
+                  _NORMS[norm], eps, base)
+
+
+def _rope_tokens(rope, t, name, contiguous):
+    """(pointer, elements between tokens, frames) of bf16 tokens [..., H, d] whose leading
+    dimensions are frames x tokens at one stride."""
+    what = "lf_rope"
+    if not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{what}: {name} must be a bf16 CUDA tensor")
+    T = rope.height * rope.width
+    if t.dim() < 3 or tuple(t.shape[-2:]) != (rope.H, rope.d) or t.numel() % (T * rope.H * rope.d):
+        raise ValueError(f"{what}: {name} must be [frames, {T}, {rope.H}, {rope.d}] or "
+                         f"[frames * {T}, {rope.H}, {rope.d}]")
+    n = t.numel() // (rope.H * rope.d)
+    stride = rope.H * rope.d
+    sizes = [(s, st) for s, st in zip(t.shape[:-2], t.stride()[:-2]) if s != 1]
+    if sizes:
+        stride = sizes[-1][1]
+    step = stride
+    for s, st in reversed(sizes):
+        if st != step:
+            raise ValueError(f"{what}: {name}'s tokens are not at one stride")
+        step *= s
+    if (t.stride(-1) != 1 and rope.d > 1) or (t.stride(-2) != rope.d and rope.H > 1):
+        raise ValueError(f"{what}: a token's H * d channels of {name} must be contiguous")
+    if contiguous and stride != rope.H * rope.d:
+        raise ValueError(f"{what}: {name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), stride, n // T
+
+
+def _frames(rope, v, name):
+    if v is None:
+        return None, None
+    if len(v) != rope.n_frames:
+        raise ValueError(f"lf_rope: {name} needs one entry per frame")
+    return _slots(v)
+
+
+def _rope_weight(rope, device, **tensors):
+    n = rope.d if rope.norm == 1 else rope.H * rope.d
+    _on(device, "lf_rope", torch.float32, n, **tensors)
+
+
+def lf_rope_frames(rope, x, out, frame_pos=None, weight=None, in_slots=None, out_slots=None,
+                   stream=None):
+    """Norm and rotary positions of n_frames frames of x [n_in, T, H, d] (tokens may lie
+    inside a wider projection) into out [n_out, T, H, d], through optional slot lists."""
+    px, xs, n_in = _rope_tokens(rope, x, "x", False)
+    po, _, n_out = _rope_tokens(rope, out, "out", True)
+    _rope_weight(rope, x.device, weight=weight)
+    _on(x.device, "lf_rope", torch.bfloat16, None, out=out)
+    si, _k1 = _frames(rope, in_slots, "in_slots")
+    so, _k2 = _frames(rope, out_slots, "out_slots")
+    fp, _k3 = _frames(rope, frame_pos, "frame_pos")
+    with torch.cuda.device(x.device):
+        _check(load().lf_rope_frames(ctypes.byref(rope), px, xs, n_in, si, fp, _ptr(weight), po,
+                                     n_out, so, _stream(stream)), "lf_rope_frames")
+
+
+def lf_rope_backward_workspace_size(rope) -> int:
+    return int(load().lf_rope_backward_workspace_size(ctypes.byref(rope)))
+
+
+def lf_rope_frames_backward(rope, x, dout, dx, frame_pos=None, weight=None, dweight=None,
+                            in_slots=None, out_slots=None, workspace=None, stream=None):
+    """Gradient of lf_rope_frames: dx (x's frames and slots, its own token stride) and, with a
+    norm, dweight, from dout.  x may be None without a norm."""
+    px, xs = None, 0
+    pd, ds, n_in = _rope_tokens(rope, dx, "dx", False)
+    if x is not None:
+        px, xs, n_x = _rope_tokens(rope, x, "x", False)
+        if n_x != n_in:
+            raise ValueError("lf_rope: x and dx differ in frames")
+    pg, _, n_out = _rope_tokens(rope, dout, "dout", True)
+    _rope_weight(rope, dx.device, weight=weight, dweight=dweight)
+    _on(dx.device, "lf_rope", torch.bfloat16, None, x=x, dout=dout)
+    si, _k1 = _frames(rope, in_slots, "in_slots")
+    so, _k2 = _frames(rope, out_slots, "out_slots")
+    fp, _k3 = _frames(rope, frame_pos, "frame_pos")
+    with torch.cuda.device(dx.device):
+        workspace, size = _workspace(workspace, lf_rope_backward_workspace_size(rope), dx.device,
+                                     stream)
+        _on(dx.device, "lf_rope", torch.uint8, None, workspace=workspace)
+        _check(load().lf_rope_frames_backward(
+            ctypes.byref(rope), px, xs, n_in, si, fp, _ptr(weight), pg, n_out, so, pd, ds,
+            _ptr(dweight), _ptr(workspace), size, _stream(stream)), "lf_rope_frames_backward")

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <string.h>
 
@@ -14,6 +15,8 @@
 #include "lf_attn.cuh"
 #include "lf_fused.cuh"
 #include "lf_fp8.cuh"
+#include "lf_attn_bwd.cuh"
+#include "lf_rope.cuh"
 
 using lf::Dims;
 
@@ -457,6 +460,205 @@ int run_select_current(const Dims& D, const void* q, const void* k_cur, const Fw
   return launch_select_current(D, w.q_blk, w.kc_blk, cur_idx, stream);
 }
 
+// ---------------------------------------------------------------- attention gradient
+struct BwdWs {
+  AttnWs attn;
+  lf::BwdRows rows;
+  uint32_t* inv;
+  int32_t *inv_total, *inv_off, *inv_cnt;
+  size_t bytes;
+};
+
+// forward attention workspace (key plans, partial dq of split tiles) | rows | transposed plans
+BwdWs carve_bwd(const Dims& D, void* base, int n_sm) {
+  BwdWs w{};
+  w.attn = carve_attn(D, base, n_sm);
+  uint8_t* p = static_cast<uint8_t*>(base);
+  size_t off = w.attn.bytes;
+  auto take = [&](size_t n) { uint8_t* r = p ? p + off : nullptr; off += align_up(n, 256); return r; };
+  const lf::KeyTiles K = lf::key_tiles(D, true);
+  const bool lists = K.n_list() > 0;
+  const size_t dense = (size_t)D.H * lf::bwd_dense_rows(D) * sizeof(float);
+  const size_t blk = lists ? (size_t)D.H * lf::bwd_blk_rows(D) * sizeof(float) : 0;
+  w.rows.dense_nlse = reinterpret_cast<float*>(take(dense));
+  w.rows.dense_nd = reinterpret_cast<float*>(take(dense));
+  w.rows.blk_nlse = reinterpret_cast<float*>(take(blk));
+  w.rows.blk_nd = reinterpret_cast<float*>(take(blk));
+  w.inv_total = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
+  w.inv_off = reinterpret_cast<int32_t*>(take((size_t)K.n_list() * D.H * sizeof(int32_t)));
+  w.inv_cnt = reinterpret_cast<int32_t*>(take((size_t)K.n_list() * D.H * sizeof(int32_t)));
+  w.inv = reinterpret_cast<uint32_t*>(take((size_t)D.H * D.nqb * (D.nsel + D.kc) * sizeof(uint32_t)));
+  w.bytes = off;
+  return w;
+}
+
+// The gradient's own limits: launch and list indices are 32-bit.
+int check_bwd_dims(const Dims& D) {
+  const lf::KeyTiles K = lf::key_tiles(D, true);
+  const long long tiles = (long long)K.n_dense + K.n_sink + (long long)K.n_list();
+  const long long rows = (long long)D.nqb * D.B + 128;
+  if (tiles * D.H > INT32_MAX / 2 || rows > INT32_MAX / 2 || rows * D.H * (D.d / 8) > (1LL << 38) ||
+      (long long)D.H * D.nqb * (D.nsel + D.kc) > INT32_MAX / 2 || D.H > 65535)
+    return LF_ERR_UNSUPPORTED;
+  return LF_OK;
+}
+
+struct BwdPtrs {
+  const void *q, *k_cur, *v_cur, *k_cache, *v_cache, *out, *dout;
+  const float* lse;
+  void *dq, *dk_cur, *dv_cur, *dk_cache, *dv_cache;
+};
+
+int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
+                    const int32_t* sink_slots, const int32_t* block_idx, const int32_t* cur_idx,
+                    void* workspace, cudaStream_t st) {
+  const int n_sm = sm_count();
+  if (n_sm <= 0) return LF_ERR_CUDA;
+  const BwdWs w = carve_bwd(D, workspace, n_sm);
+  const bool cache_grad = b.dk_cache != nullptr;
+  lf::BwdRows rows = w.rows;
+  const lf::KeyTiles K = lf::key_tiles(D, cache_grad);
+  {
+    const long long items = ((long long)lf::bwd_blk_rows(D) + lf::bwd_dense_rows(D) - D.ncur) * D.H;
+    const long long threads = items * (D.d / 8);
+    lf::bwd_rows_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
+        static_cast<const __nv_bfloat16*>(b.out), static_cast<const __nv_bfloat16*>(b.dout), b.lse,
+        rows, w.inv_total, lf::key_tiles(D, true).n_list() > 0, D);
+  }
+  lf::plan_kernel<<<dim3(lf::cdiv(lf::tile_count(D), lf::kPlanWarps), D.H), lf::kPlanWarps * 32, 0, st>>>(
+      D.F > 0 ? block_idx : nullptr, D.kc > 0 ? cur_idx : nullptr, w.attn.plan, w.attn.plan_cnt, D);
+  if (K.n_list() > 0)
+    lf::bwd_transpose_kernel<<<lf::cdiv(K.n_list() * D.H, lf::kInvWarps), lf::kInvWarps * 32, 0, st>>>(
+        w.attn.plan, w.attn.plan_cnt, K, w.inv, w.inv_total, w.inv_off, w.inv_cnt, D);
+  int rc = cuda_status(cudaGetLastError());
+  if (rc != LF_OK) return rc;
+  lf::BwdArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = static_cast<const __nv_bfloat16*>(b.q);
+  a.k_cur = static_cast<const __nv_bfloat16*>(b.k_cur);
+  a.v_cur = static_cast<const __nv_bfloat16*>(b.v_cur);
+  a.k_cache = static_cast<const __nv_bfloat16*>(b.k_cache);
+  a.v_cache = static_cast<const __nv_bfloat16*>(b.v_cache);
+  a.dout = static_cast<const __nv_bfloat16*>(b.dout);
+  a.dq = static_cast<__nv_bfloat16*>(b.dq);
+  a.dk_cur = static_cast<__nv_bfloat16*>(b.dk_cur);
+  a.dv_cur = static_cast<__nv_bfloat16*>(b.dv_cur);
+  a.dk_cache = static_cast<__nv_bfloat16*>(b.dk_cache);
+  a.dv_cache = static_cast<__nv_bfloat16*>(b.dv_cache);
+  a.plan = w.attn.plan;
+  a.plan_cnt = w.attn.plan_cnt;
+  a.rows = rows;
+  a.kt = K;
+  a.inv = w.inv;
+  a.inv_off = w.inv_off;
+  a.inv_cnt = w.inv_cnt;
+  for (int i = 0; i < D.S; ++i) a.slots[i] = sink_slots[i];
+  for (int i = 0; i < D.F; ++i) a.slots[D.S + i] = hist_slots[i];
+  auto dq = D.d == 128 ? lf::bwd_dq_simple_kernel<128> : lf::bwd_dq_simple_kernel<64>;
+  auto dkv = D.d == 128 ? lf::bwd_dkv_simple_kernel<128> : lf::bwd_dkv_simple_kernel<64>;
+  dq<<<dim3(lf::cdiv(D.ncur, 8), D.H), 256, 0, st>>>(a, D);
+  dkv<<<dim3(K.total() * D.H, 16), 256, 0, st>>>(a, D);
+  return cuda_status(cudaGetLastError());
+}
+
+// ---------------------------------------------------------------- rotary positions
+// Validates a rotary call's sizes and lists and fills the kernel's arguments but for the
+// tensors.  Lists are host arrays of n_frames, or null for 0, 1, ...
+int make_rope(const lf_rope* r, int32_t n_in, const int32_t* in_slots, const int32_t* frame_pos,
+              int32_t n_out, const int32_t* out_slots, lf::RopeArgs* A) {
+  if (r == nullptr) return LF_ERR_INVALID_ARG;
+  if (r->d != 64 && r->d != 128) return LF_ERR_UNSUPPORTED;
+  if (r->H < 1 || r->n_frames < 1 || r->height < 1 || r->width < 1 || r->pairs_t < 0 ||
+      r->pairs_h < 0 || r->pairs_w < 0 || (r->halves != 0 && r->halves != 1) ||
+      r->norm < LF_NORM_NONE || r->norm > LF_NORM_TOKEN)
+    return LF_ERR_INVALID_ARG;
+  if ((long long)r->H * r->d > LF_MAX_ROPE_CHANNELS || r->n_frames > LF_MAX_FRAMES ||
+      (long long)r->height * r->width > (1 << 24))
+    return LF_ERR_UNSUPPORTED;
+  if ((long long)r->pairs_t + r->pairs_h + r->pairs_w > r->d / 2) return LF_ERR_INVALID_ARG;
+  if (!(r->base > 0.0) || !std::isfinite(r->base) || !(r->eps >= 0.f) || !std::isfinite(r->eps))
+    return LF_ERR_INVALID_ARG;
+  if (n_in < 1 || n_out < 1 || (in_slots == nullptr && n_in < r->n_frames) ||
+      (out_slots == nullptr && n_out < r->n_frames))
+    return LF_ERR_INVALID_ARG;
+  A->H = r->H;
+  A->d = r->d;
+  A->T = r->height * r->width;
+  A->width = r->width;
+  A->n_tokens = (int64_t)r->n_frames * A->T;
+  if ((int64_t)(n_in > n_out ? n_in : n_out) * A->T > ((int64_t)1 << 40) / (r->H * r->d))
+    return LF_ERR_UNSUPPORTED;
+  int rc;
+  if (in_slots != nullptr && (rc = check_slots(in_slots, r->n_frames, n_in)) != LF_OK) return rc;
+  if (out_slots != nullptr && (rc = check_slots(out_slots, r->n_frames, n_out)) != LF_OK) return rc;
+  for (int f = 0; f < r->n_frames; ++f) {
+    A->x_slot[f] = in_slots != nullptr ? in_slots[f] : f;
+    A->out_slot[f] = out_slots != nullptr ? out_slots[f] : f;
+    A->pos[f] = frame_pos != nullptr ? frame_pos[f] : f;
+  }
+  A->p_t = r->pairs_t;
+  A->p_h = A->p_t + r->pairs_h;
+  A->p_w = A->p_h + r->pairs_w;
+  for (int p = 0; p < A->p_w; ++p) {
+    const int n = p < A->p_t ? r->pairs_t : p < A->p_h ? r->pairs_h : r->pairs_w;
+    const int i = p < A->p_t ? p : p < A->p_h ? p - A->p_t : p - A->p_h;
+    A->turns[p] = std::pow(r->base, -(double)i / n) / 6.283185307179586477;
+  }
+  A->halves = r->halves;
+  A->norm = r->norm;
+  A->eps = r->eps;
+  A->sign = 1.f;
+  A->inv_n = 1.f / (float)(r->norm == LF_NORM_HEAD ? r->d : r->H * r->d);
+  A->upd = r->d / 16;
+  A->units = r->H * A->upd;
+  // threads per token: the fewest lanes (a power of two, whole heads) that hold it in one
+  // unit each, else a warp with up to kRopeUnits units per lane, else several warps
+  if (A->units <= 32) {
+    A->tpt = A->upd;
+    while (A->tpt < A->units) A->tpt *= 2;
+  } else {
+    A->tpt = 32 * lf::cdiv(A->units, 32 * lf::kRopeUnits);
+  }
+  A->groups = lf::kRopeThreads / A->tpt;
+  return LF_OK;
+}
+
+// No slot twice among n (each < n_slots, checked before).
+bool slots_distinct(const int32_t* a, int na, const int32_t* b, int nb) {
+  for (int i = 0; i < na + nb; ++i)
+    for (int j = 0; j < i; ++j)
+      if ((i < na ? a[i] : b[i - na]) == (j < na ? a[j] : b[j - na])) return false;
+  return true;
+}
+
+size_t rope_smem(const lf::RopeArgs& A, bool bwd) {
+  return (size_t)A.groups * (A.d / 2) * sizeof(float2) + 32 * sizeof(float) +
+         (bwd ? (size_t)(A.norm == LF_NORM_TOKEN ? A.H * A.d : A.d) * sizeof(float) : 0);
+}
+
+int launch_rope(const lf::RopeArgs& A, cudaStream_t st) {
+  const int64_t grid = (A.n_tokens + A.groups - 1) / A.groups;
+  if (grid > INT32_MAX) return LF_ERR_UNSUPPORTED;
+  const int u = lf::cdiv(A.units, A.tpt);
+  auto kern = u == 1 ? lf::rope_kernel<1> : u == 2 ? lf::rope_kernel<2> : lf::rope_kernel<3>;
+  kern<<<(unsigned)grid, A.tpt * A.groups, rope_smem(A, false), st>>>(A);
+  return cuda_status(cudaGetLastError());
+}
+
+int launch_rope_bwd(const lf::RopeArgs& A, float* dweight, cudaStream_t st) {
+  const int u = lf::cdiv(A.units, A.tpt);
+  auto kern = u == 1 ? lf::rope_bwd_kernel<1> : u == 2 ? lf::rope_bwd_kernel<2> : lf::rope_bwd_kernel<3>;
+  const size_t smem = rope_smem(A, true);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return LF_ERR_CUDA;
+  const int64_t steps = (A.n_tokens + A.groups - 1) / A.groups;
+  const int grid = (int)std::min<int64_t>(steps, lf::kRopeBwdCtas);
+  const int n_dw = A.norm == LF_NORM_TOKEN ? A.H * A.d : A.d;
+  kern<<<grid, A.tpt * A.groups, smem, st>>>(A);
+  lf::rope_dweight_kernel<<<lf::cdiv(n_dw, 32), 512, 0, st>>>(A.part, grid, n_dw, dweight);
+  return cuda_status(cudaGetLastError());
+}
+
 // ---------------------------------------------------------------- fixed scratch
 // Scratch for lf_block_sparse_attn_noalloc: a fixed-size array in device global memory.
 // It exists on a device once this library's module is loaded there (with lazy module
@@ -688,6 +890,121 @@ int lf_block_sparse_attn_e4m3(const lf_shape* shape, const void* q8, const float
   const F8Args f8{q8, q_scale, k_cur8, k_cache8, k_scale};
   return launch_attn(D, nullptr, nullptr, v_cur, nullptr, v_cache, hist_slots, sink_slots,
                      block_idx, cur_idx, out, lse, workspace, stream, false, &f8);
+}
+
+size_t lf_attn_backward_workspace_size(const lf_shape* shape) {
+  Dims D;
+  if (make_dims(shape, &D) != LF_OK || check_bwd_dims(D) != LF_OK) return 0;
+  return carve_bwd(D, nullptr, sm_count()).bytes;
+}
+
+int lf_block_sparse_attn_backward(const lf_shape* shape, const void* q, const void* k_cur,
+                                  const void* v_cur, const void* k_cache, const void* v_cache,
+                                  const int32_t* hist_slots, const int32_t* sink_slots,
+                                  const int32_t* block_idx, const int32_t* cur_idx,
+                                  const void* out, const void* dout, const float* lse, void* dq,
+                                  void* dk_cur, void* dv_cur, void* dk_cache, void* dv_cache,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  Dims D;
+  int rc = make_dims(shape, &D);
+  if (rc != LF_OK) return rc;
+  if ((rc = check_bwd_dims(D)) != LF_OK) return rc;
+  for (const void* p : {q, k_cur, v_cur, out, dout, (const void*)dq, (const void*)dk_cur,
+                        (const void*)dv_cur})
+    if (p == nullptr || !aligned(p, 16)) return LF_ERR_INVALID_ARG;
+  if (lse == nullptr || !aligned(lse, 4)) return LF_ERR_INVALID_ARG;
+  if (D.F + D.S > 0 && (k_cache == nullptr || v_cache == nullptr || !aligned(k_cache, 16) ||
+                        !aligned(v_cache, 16)))
+    return LF_ERR_INVALID_ARG;
+  if ((dk_cache == nullptr) != (dv_cache == nullptr) ||
+      (dk_cache != nullptr && (!aligned(dk_cache, 16) || !aligned(dv_cache, 16))))
+    return LF_ERR_INVALID_ARG;
+  if (D.F > 0 && (block_idx == nullptr || !aligned(block_idx, 4))) return LF_ERR_INVALID_ARG;
+  if (D.kc > 0 && (cur_idx == nullptr || !aligned(cur_idx, 4))) return LF_ERR_INVALID_ARG;
+  if ((rc = check_slots(hist_slots, D.F, D.n_slots)) != LF_OK) return rc;
+  if ((rc = check_slots(sink_slots, D.S, D.n_slots)) != LF_OK) return rc;
+  if (dk_cache != nullptr && !slots_distinct(hist_slots, D.F, sink_slots, D.S))
+    return LF_ERR_INVALID_ARG;
+  const size_t need = carve_bwd(D, nullptr, sm_count()).bytes;
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need)
+    return LF_ERR_WORKSPACE;
+  const BwdPtrs b{q, k_cur, v_cur, k_cache, v_cache, out, dout, lse, dq, dk_cur, dv_cur,
+                  dk_cache, dv_cache};
+  return launch_attn_bwd(D, b, hist_slots, sink_slots, block_idx, cur_idx, workspace, stream);
+}
+
+int lf_rope_frames(const lf_rope* rope, const void* x, int64_t x_stride, int32_t n_in,
+                   const int32_t* in_slots, const int32_t* frame_pos, const float* weight,
+                   void* out, int32_t n_out, const int32_t* out_slots, cudaStream_t stream) {
+  lf::RopeArgs A;
+  memset(&A, 0, sizeof(A));
+  int rc = make_rope(rope, n_in, in_slots, frame_pos, n_out, out_slots, &A);
+  if (rc != LF_OK) return rc;
+  if (x == nullptr || out == nullptr || !aligned(x, 16) || !aligned(out, 16) ||
+      x_stride < (int64_t)A.H * A.d || x_stride % 8 != 0 || x_stride > ((int64_t)1 << 32) ||
+      (weight != nullptr) != (A.norm != LF_NORM_NONE) || !aligned(weight, 16))
+    return LF_ERR_INVALID_ARG;
+  if (!slots_distinct(A.out_slot, rope->n_frames, nullptr, 0)) return LF_ERR_INVALID_ARG;
+  A.x = static_cast<const __nv_bfloat16*>(x);
+  A.x_stride = x_stride;
+  A.weight = weight;
+  A.out = static_cast<__nv_bfloat16*>(out);
+  A.out_stride = (int64_t)A.H * A.d;
+  return launch_rope(A, stream);
+}
+
+size_t lf_rope_backward_workspace_size(const lf_rope* rope) {
+  lf::RopeArgs A;
+  if (rope == nullptr || make_rope(rope, rope->n_frames, nullptr, nullptr, rope->n_frames, nullptr,
+                                   &A) != LF_OK || A.norm == LF_NORM_NONE)
+    return 0;
+  return align_up((size_t)lf::kRopeBwdCtas * (A.norm == LF_NORM_TOKEN ? A.H * A.d : A.d) *
+                  sizeof(float), 256);
+}
+
+int lf_rope_frames_backward(const lf_rope* rope, const void* x, int64_t x_stride, int32_t n_in,
+                            const int32_t* in_slots, const int32_t* frame_pos,
+                            const float* weight, const void* dout, int32_t n_out,
+                            const int32_t* out_slots, void* dx, int64_t dx_stride,
+                            float* dweight, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  lf::RopeArgs A;
+  memset(&A, 0, sizeof(A));
+  int rc = make_rope(rope, n_in, in_slots, frame_pos, n_out, out_slots, &A);
+  if (rc != LF_OK) return rc;
+  const int64_t row = (int64_t)A.H * A.d;
+  const bool norm = A.norm != LF_NORM_NONE;
+  if (dout == nullptr || dx == nullptr || !aligned(dout, 16) || !aligned(dx, 16) ||
+      dx_stride < row || dx_stride % 8 != 0 || dx_stride > ((int64_t)1 << 32) ||
+      (dweight != nullptr) != norm || !aligned(dweight, 4))
+    return LF_ERR_INVALID_ARG;
+  if (norm && (x == nullptr || !aligned(x, 16) || x_stride < row || x_stride % 8 != 0 ||
+               x_stride > ((int64_t)1 << 32) || weight == nullptr || !aligned(weight, 16)))
+    return LF_ERR_INVALID_ARG;
+  if (!slots_distinct(A.x_slot, rope->n_frames, nullptr, 0) ||
+      !slots_distinct(A.out_slot, rope->n_frames, nullptr, 0))
+    return LF_ERR_INVALID_ARG;
+  A.sign = -1.f;
+  A.out = static_cast<__nv_bfloat16*>(dx);
+  A.out_stride = dx_stride;
+  if (!norm) {                  // R is orthogonal: the forward kernel with the angles negated
+    std::swap(A.x_slot, A.out_slot);
+    A.x = static_cast<const __nv_bfloat16*>(dout);
+    A.x_stride = row;
+    return launch_rope(A, stream);
+  }
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < lf_rope_backward_workspace_size(rope))
+    return LF_ERR_WORKSPACE;
+  memcpy(A.dout_slot, A.out_slot, sizeof(A.dout_slot));
+  memcpy(A.out_slot, A.x_slot, sizeof(A.out_slot));
+  A.x = static_cast<const __nv_bfloat16*>(x);
+  A.x_stride = x_stride;
+  A.dout = static_cast<const __nv_bfloat16*>(dout);
+  A.dout_stride = row;
+  A.weight = weight;
+  A.part = static_cast<float*>(workspace);
+  return launch_rope_bwd(A, dweight, stream);
 }
 
 int lf_quantize_e4m3(const void* x, int64_t rows, int32_t H, int32_t d, const float* head_scale,

@@ -78,6 +78,7 @@ extern "C" {
 #define LF_MAX_PLAN         2048    /* key blocks per 128-row query tile:
                                        n_sink * n_bpf + (block == 64 ? 2 : 1) * (kc + kf*kb) */
 #define LF_MAX_CUR_BLOCKS   256     /* n_qb when the current chunk is sparse (k_c > 0)    */
+#define LF_MAX_ROPE_CHANNELS 12288  /* H * d of lf_rope                                   */
 
 typedef struct lf_shape {
     int32_t H;                /* heads, >= 1                                              */
@@ -206,6 +207,89 @@ int lf_block_sparse_attn(const lf_shape* shape, const void* q, const void* k_cur
                          const int32_t* block_idx, const int32_t* cur_idx, void* out,
                          float* lse, void* workspace, size_t workspace_bytes,
                          cudaStream_t stream);
+
+/* Gradient of (d), for training through the attention of a chunk [LF-gist 2.2 "execution"
+ * defines the attention; the pages give no gradient, this is the formulas' own].  With P =
+ * exp(scale q.k - lse) recomputed from the forward call's lse, dP = dout . v and D = dout . out
+ * per row:
+ *   dS = P (dP - D),  dq = scale sum_k dS k,  dk = scale sum_q dS q,  dv = sum_q P dout,
+ * over exactly the (query, key) pairs that lf_block_sparse_attn attends to with the same
+ * lists (also when it drops an invalid one).  The selection itself has no gradient.
+ * q ... cur_idx, out, lse: the arguments and results of the forward call (out bf16, lse fp32,
+ * both required); dout: bf16, q's layout.  dq, dk_cur, dv_cur: bf16, q's layout, written
+ * whole.  dk_cache, dv_cache: bf16, the cache's layout, both NULL (no gradient into the
+ * cache: the cached frames were detached) or both given: then every row of the slots in
+ * sink_slots and hist_slots is written (zero where no query attends to it), other slots are
+ * left as they were, and a slot listed twice is LF_ERR_INVALID_ARG (its two gradients would
+ * meet in one place).  Outputs must not overlap inputs or each other.  A row that attends to
+ * nothing (lse = -inf) gets dq = 0 and gives nothing to dk and dv.  Products run on bf16
+ * tensor cores with P and dS rounded to bf16, sums in fp32; each gradient is rounded once.
+ * workspace: at least lf_attn_backward_workspace_size(shape) bytes, 256-byte aligned, for
+ * this call alone until it has finished on the GPU.  LF_ERR_BAD_INDEX and LF_ERR_TIMEOUT as
+ * for lf_block_sparse_attn. */
+size_t lf_attn_backward_workspace_size(const lf_shape* shape);
+int lf_block_sparse_attn_backward(const lf_shape* shape, const void* q, const void* k_cur,
+                                  const void* v_cur, const void* k_cache, const void* v_cache,
+                                  const int32_t* hist_slots, const int32_t* sink_slots,
+                                  const int32_t* block_idx, const int32_t* cur_idx,
+                                  const void* out, const void* dout, const float* lse, void* dq,
+                                  void* dk_cur, void* dv_cur, void* dk_cache, void* dv_cache,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Rotary positions with three axes, on queries and keys before they enter the attention or
+ * the cache, with the RMS norm that precedes them.  The pages describe the attention of an
+ * existing video model and take its rotated queries and keys as given; these entry points
+ * make them.  Frames are grids of height x width tokens in raster order (T = height * width,
+ * the T of lf_shape). */
+#define LF_NORM_NONE  0   /* no norm                                                       */
+#define LF_NORM_HEAD  1   /* over each head's d channels; weight [d]                       */
+#define LF_NORM_TOKEN 2   /* over a token's H * d channels; weight [H * d]                 */
+
+typedef struct lf_rope {
+    int32_t H, d;             /* heads; head dimension, 64 or 128; H*d <= LF_MAX_ROPE_CHANNELS */
+    int32_t n_frames;         /* frames per call, 1..LF_MAX_FRAMES                         */
+    int32_t height, width;    /* tokens of a frame, each >= 1, height * width <= 2^24      */
+    int32_t pairs_t, pairs_h, pairs_w;  /* channel pairs turned by the frame's position, the
+                                 token's row and its column; each >= 0, their sum <= d / 2;
+                                 pairs beyond the sum are not turned                       */
+    int32_t halves;           /* pair p is channels 0: (2p, 2p + 1), 1: (p, p + d / 2)     */
+    int32_t norm;             /* LF_NORM_*                                                 */
+    float eps;                /* added to the mean square, >= 0                            */
+    double base;              /* frequency base, > 0: pair i of an axis with n pairs turns by
+                                 position * base^(-i / n) radians                          */
+} lf_rope;
+
+/* out[frame, t, h] = R(position) (w * x * r), r = 1 / sqrt(mean(x^2) + eps) over the norm's
+ * channels (w * r = 1 without a norm), computed in fp32 (angles in fp64, so far positions
+ * lose nothing) and rounded once to bf16.
+ * x: bf16 tokens [n_in * T] of H * d contiguous channels, x_stride elements apart (a multiple
+ *   of 8, >= H * d: queries or keys inside a fused projection); frame f of the call is frame
+ *   in_slots[f] of x, or f when in_slots is NULL.  A frame may be read more than once.
+ * out: bf16 [n_out, T, H, d], contiguous; frame f goes to frame out_slots[f], or f when
+ *   out_slots is NULL; the others are left as they were.  out_slots must not repeat a slot.
+ * frame_pos: the frames' positions on the time axis, NULL: 0, 1, ...; any int32.
+ * in_slots, out_slots, frame_pos: HOST arrays of n_frames, read during the call only.
+ * weight: fp32, 16-byte aligned, for norm != LF_NORM_NONE; NULL without a norm.
+ * out may be x when strides and slots agree frame by frame; otherwise they must not overlap.
+ * Without pairs and norm the call moves frames into cache slots (values). */
+int lf_rope_frames(const lf_rope* rope, const void* x, int64_t x_stride, int32_t n_in,
+                   const int32_t* in_slots, const int32_t* frame_pos, const float* weight,
+                   void* out, int32_t n_out, const int32_t* out_slots, cudaStream_t stream);
+
+/* Gradient of lf_rope_frames.  dout: bf16 [n_out, T, H, d] with frame f at out_slots[f] (or
+ * f); dx: bf16, x's frames and slots, dx_stride elements between tokens, written at frame
+ * in_slots[f] (or f) only; a slot repeated in in_slots is LF_ERR_INVALID_ARG here.  dweight:
+ * fp32, weight's shape, written whole (sum over the call's tokens); NULL without a norm.  x
+ * and weight may be NULL without a norm.  dx may be dout when strides and slots agree.
+ * workspace: lf_rope_backward_workspace_size bytes (0 without a norm: may be NULL), 256-byte
+ * aligned. */
+size_t lf_rope_backward_workspace_size(const lf_rope* rope);
+int lf_rope_frames_backward(const lf_rope* rope, const void* x, int64_t x_stride, int32_t n_in,
+                            const int32_t* in_slots, const int32_t* frame_pos,
+                            const float* weight, const void* dout, int32_t n_out,
+                            const int32_t* out_slots, void* dx, int64_t dx_stride,
+                            float* dweight, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
 
 /* FP8 (e4m3) variant of (d) [LF-yly 五 deploys the video model with FP8, activations
  * quantised per token; using e4m3 for the attention's QK^T operands is this library's
