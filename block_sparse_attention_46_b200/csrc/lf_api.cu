@@ -478,12 +478,10 @@ BwdWs carve_bwd(const Dims& D, void* base, int n_sm) {
   auto take = [&](size_t n) { uint8_t* r = p ? p + off : nullptr; off += align_up(n, 256); return r; };
   const lf::KeyTiles K = lf::key_tiles(D, true);
   const bool lists = K.n_list() > 0;
-  const size_t dense = (size_t)D.H * lf::bwd_dense_rows(D) * sizeof(float);
-  const size_t blk = lists ? (size_t)D.H * lf::bwd_blk_rows(D) * sizeof(float) : 0;
-  w.rows.dense_nlse = reinterpret_cast<float*>(take(dense));
-  w.rows.dense_nd = reinterpret_cast<float*>(take(dense));
-  w.rows.blk_nlse = reinterpret_cast<float*>(take(blk));
-  w.rows.blk_nd = reinterpret_cast<float*>(take(blk));
+  constexpr size_t box = lf::kBoxFloats * sizeof(float);
+  w.rows.dense = reinterpret_cast<float*>(take((size_t)D.H * lf::bwd_dense_boxes(D) * box));
+  w.rows.blk = reinterpret_cast<float*>(
+      take(lists ? ((size_t)D.H * lf::bwd_blk_boxes(D) + 1) * box : 0));
   w.inv_total = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
   w.inv_off = reinterpret_cast<int32_t*>(take((size_t)K.n_list() * D.H * sizeof(int32_t)));
   w.inv_cnt = reinterpret_cast<int32_t*>(take((size_t)K.n_list() * D.H * sizeof(int32_t)));
@@ -497,7 +495,7 @@ int check_bwd_dims(const Dims& D) {
   const lf::KeyTiles K = lf::key_tiles(D, true);
   const long long tiles = (long long)K.n_dense + K.n_sink + (long long)K.n_list();
   const long long rows = (long long)D.nqb * D.B + 128;
-  if (tiles * D.H > INT32_MAX / 2 || rows > INT32_MAX / 2 || rows * D.H * (D.d / 8) > (1LL << 38) ||
+  if ((tiles + lf::tile_count(D)) * D.H > INT32_MAX / 2 || rows > INT32_MAX / 2 || rows * D.H * (D.d / 8) > (1LL << 38) ||
       (long long)D.H * D.nqb * (D.nsel + D.kc) > INT32_MAX / 2 || D.H > 65535)
     return LF_ERR_UNSUPPORTED;
   return LF_OK;
@@ -509,6 +507,16 @@ struct BwdPtrs {
   void *dq, *dk_cur, *dv_cur, *dk_cache, *dv_cache;
 };
 
+template <int HD, int BLK>
+int launch_bwd_t(const Dims& D, const lf::BwdParams& p, int grid, cudaStream_t st) {
+  auto kern = lf::attn_bwd_kernel<HD, BLK>;
+  constexpr int smem = lf::BwdLayout<HD>::kBytes;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return LF_ERR_CUDA;
+  kern<<<grid, lf::kBwdThreads, smem, st>>>(p, D);
+  return cuda_status(cudaGetLastError());
+}
+
 int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
                     const int32_t* sink_slots, const int32_t* block_idx, const int32_t* cur_idx,
                     void* workspace, cudaStream_t st) {
@@ -519,7 +527,7 @@ int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
   lf::BwdRows rows = w.rows;
   const lf::KeyTiles K = lf::key_tiles(D, cache_grad);
   {
-    const long long items = ((long long)lf::bwd_blk_rows(D) + lf::bwd_dense_rows(D) - D.ncur) * D.H;
+    const long long items = ((long long)D.nqb * D.B + lf::bwd_dense_boxes(D) * 64 - D.ncur) * D.H;
     const long long threads = items * (D.d / 8);
     lf::bwd_rows_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
         static_cast<const __nv_bfloat16*>(b.out), static_cast<const __nv_bfloat16*>(b.dout), b.lse,
@@ -532,33 +540,44 @@ int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
         w.attn.plan, w.attn.plan_cnt, K, w.inv, w.inv_total, w.inv_off, w.inv_cnt, D);
   int rc = cuda_status(cudaGetLastError());
   if (rc != LF_OK) return rc;
-  lf::BwdArgs a;
-  memset(&a, 0, sizeof(a));
-  a.q = static_cast<const __nv_bfloat16*>(b.q);
-  a.k_cur = static_cast<const __nv_bfloat16*>(b.k_cur);
-  a.v_cur = static_cast<const __nv_bfloat16*>(b.v_cur);
-  a.k_cache = static_cast<const __nv_bfloat16*>(b.k_cache);
-  a.v_cache = static_cast<const __nv_bfloat16*>(b.v_cache);
-  a.dout = static_cast<const __nv_bfloat16*>(b.dout);
-  a.dq = static_cast<__nv_bfloat16*>(b.dq);
-  a.dk_cur = static_cast<__nv_bfloat16*>(b.dk_cur);
-  a.dv_cur = static_cast<__nv_bfloat16*>(b.dv_cur);
-  a.dk_cache = static_cast<__nv_bfloat16*>(b.dk_cache);
-  a.dv_cache = static_cast<__nv_bfloat16*>(b.dv_cache);
-  a.plan = w.attn.plan;
-  a.plan_cnt = w.attn.plan_cnt;
-  a.rows = rows;
-  a.kt = K;
-  a.inv = w.inv;
-  a.inv_off = w.inv_off;
-  a.inv_cnt = w.inv_cnt;
-  for (int i = 0; i < D.S; ++i) a.slots[i] = sink_slots[i];
-  for (int i = 0; i < D.F; ++i) a.slots[D.S + i] = hist_slots[i];
-  auto dq = D.d == 128 ? lf::bwd_dq_simple_kernel<128> : lf::bwd_dq_simple_kernel<64>;
-  auto dkv = D.d == 128 ? lf::bwd_dkv_simple_kernel<128> : lf::bwd_dkv_simple_kernel<64>;
-  dq<<<dim3(lf::cdiv(D.ncur, 8), D.H), 256, 0, st>>>(a, D);
-  dkv<<<dim3(K.total() * D.H, 16), 256, 0, st>>>(a, D);
-  return cuda_status(cudaGetLastError());
+  lf::BwdParams p;
+  memset(&p, 0, sizeof(p));
+  const int HD = D.H * D.d;
+  const struct { CUtensorMap *m2, *m3; const void* base; } chunk[4] = {
+      {&p.q2, &p.q3, b.q}, {&p.g2, &p.g3, b.dout}, {&p.kc2, &p.kc3, b.k_cur}, {&p.vc2, &p.vc3, b.v_cur}};
+  for (const auto& m : chunk) {
+    if ((rc = encode_rows(m.m2, m.base, HD, D.ncur, 0)) != LF_OK) return rc;
+    if ((rc = encode_rows(m.m3, m.base, HD, D.T, D.Fc)) != LF_OK) return rc;
+  }
+  if (D.F + D.S > 0) {
+    if ((rc = encode_rows(&p.kh, b.k_cache, HD, D.T, D.n_slots)) != LF_OK) return rc;
+    if ((rc = encode_rows(&p.vh, b.v_cache, HD, D.T, D.n_slots)) != LF_OK) return rc;
+  } else {   // never used
+    p.kh = p.kc3;
+    p.vh = p.vc3;
+  }
+  p.dq = static_cast<__nv_bfloat16*>(b.dq);
+  p.dk_cur = static_cast<__nv_bfloat16*>(b.dk_cur);
+  p.dv_cur = static_cast<__nv_bfloat16*>(b.dv_cur);
+  p.dk_cache = static_cast<__nv_bfloat16*>(b.dk_cache);
+  p.dv_cache = static_cast<__nv_bfloat16*>(b.dv_cache);
+  p.plan = w.attn.plan;
+  p.plan_cnt = w.attn.plan_cnt;
+  p.rows = rows;
+  p.kt = K;
+  p.inv = w.inv;
+  p.inv_off = w.inv_off;
+  p.inv_cnt = w.inv_cnt;
+  p.n_dq = lf::tile_count(D) * D.H;
+  p.wait_limit_ns = g_dbg_wait_limit_ns;
+  p.debug_stall = g_dbg_stall;
+  for (int i = 0; i < D.S; ++i) p.slots[i] = sink_slots[i];
+  for (int i = 0; i < D.F; ++i) p.slots[D.S + i] = hist_slots[i];
+  const int grid = p.n_dq + K.total() * D.H;
+  return D.d == 128 ? (D.B == 64 ? launch_bwd_t<128, 64>(D, p, grid, st)
+                                 : launch_bwd_t<128, 128>(D, p, grid, st))
+                    : (D.B == 64 ? launch_bwd_t<64, 64>(D, p, grid, st)
+                                 : launch_bwd_t<64, 128>(D, p, grid, st));
 }
 
 // ---------------------------------------------------------------- rotary positions

@@ -14,18 +14,20 @@
 namespace lf {
 
 // ---------------------------------------------------------------------------------
-// Rows: what the gradient needs of every query row, -lse * log2(e) and -D, padded so that
-// whole tiles can be read: `dense` rows in token order, [H, pad128(ncur)], and `blk` rows by
-// query block, [H, nqb * B] (only where some key tile has a list of query blocks).  Padding rows and rows that attend to nothing hold -inf, which
-// makes their P zero.
+// Rows: what the gradient needs of every query row, -lse * log2(e) and -D, in boxes of 64
+// rows (64 floats of the one, then 64 of the other; one 512-byte bulk copy): `dense` boxes
+// in token order, [H, 2 * ceil(ncur / 128)], and, only where some key tile has a list of
+// query blocks, `blk` boxes by query block, [H, nqb * B / 64] and one box of padding.
+// Padding rows and rows that attend to nothing hold -inf, which makes their P zero.
 // ---------------------------------------------------------------------------------
+constexpr int kBoxFloats = 128;
+
 struct BwdRows {
-  float *dense_nlse, *dense_nd;    // [H, pad128(ncur)]
-  float *blk_nlse, *blk_nd;        // [H, nqb * B]
+  float *dense, *blk;
 };
 
-__host__ __device__ inline int bwd_dense_rows(const Dims& D) { return cdiv(D.ncur, 128) * 128; }
-__host__ __device__ inline int bwd_blk_rows(const Dims& D) { return D.nqb * D.B; }
+__host__ __device__ inline int bwd_dense_boxes(const Dims& D) { return cdiv(D.ncur, 128) * 2; }
+__host__ __device__ inline int bwd_blk_boxes(const Dims& D) { return D.nqb * (D.B / 64); }
 
 // d / 8 threads per (row, head), 16-byte loads, heads fastest (a token's row is contiguous).
 // Also zeroes the entry counter of the transposed plans.
@@ -34,11 +36,14 @@ bwd_rows_kernel(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __re
                 const float* __restrict__ lse, BwdRows R, int32_t* inv_total, bool blk,
                 const Dims D) {
   if (blockIdx.x == 0 && threadIdx.x == 0) *inv_total = 0;
+  if (blk && blockIdx.x == 0 && threadIdx.x < kBoxFloats)
+    R.blk[(size_t)D.H * bwd_blk_boxes(D) * kBoxFloats + threadIdx.x] =
+        threadIdx.x < 64 ? -INFINITY : 0.f;
   const int per = D.d / 8;
   const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long item = idx / per;
   const int part = (int)(idx % per);
-  const int blk_rows = bwd_blk_rows(D), dense_rows = bwd_dense_rows(D);
+  const int blk_rows = D.nqb * D.B, dense_rows = bwd_dense_boxes(D) * 64;
   const long long p = item / D.H;                        // padded row; then the dense padding
   const int h = (int)(item % D.H);
   int tok = -1;
@@ -65,19 +70,16 @@ bwd_rows_kernel(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __re
     const float l = lse[(size_t)h * D.ncur + tok];
     if (l != -INFINITY) nl = -l * 1.4426950408889634f;
   }
+  auto put = [&](float* base, size_t box0, int row) {
+    float* b = base + (box0 + row / 64) * kBoxFloats + row % 64;
+    b[0] = nl;
+    b[64] = -s;
+  };
   if (p < blk_rows) {
-    if (blk) {
-      R.blk_nlse[(size_t)h * blk_rows + p] = nl;
-      R.blk_nd[(size_t)h * blk_rows + p] = -s;
-    }
-    if (tok >= 0) {
-      R.dense_nlse[(size_t)h * dense_rows + tok] = nl;
-      R.dense_nd[(size_t)h * dense_rows + tok] = -s;
-    }
+    if (blk) put(R.blk, (size_t)h * bwd_blk_boxes(D), (int)p);
+    if (tok >= 0) put(R.dense, (size_t)h * bwd_dense_boxes(D), tok);
   } else if (p - blk_rows < dense_rows - D.ncur) {
-    const size_t at = (size_t)h * dense_rows + D.ncur + (size_t)(p - blk_rows);
-    R.dense_nlse[at] = -INFINITY;
-    R.dense_nd[at] = 0.f;
+    put(R.dense, (size_t)h * bwd_dense_boxes(D), D.ncur + (int)(p - blk_rows));
   }
 }
 
@@ -221,10 +223,28 @@ bwd_transpose_kernel(const uint32_t* __restrict__ plan, const int32_t* __restric
 }
 
 // ---------------------------------------------------------------------------------
-// The two passes, one warp per output row; each lane holds d / 32 channels.
+// The two passes, in one launch: CTAs [0, tiles * H) take a (head, 128-row query tile) each
+// and give dq, the others a key tile each and give dk and dv.  A CTA keeps its own two
+// operand tiles in shared memory (Q and dout; K and V) and streams the other side's through
+// two rings; its accumulators stay in tensor memory until the end.
+//
+//   dq:      S = Q K^T, dP = dout V^T, dS = P (dP - D) as bf16 over S, dq += dS K
+//   dk, dv:  S^T = K Q^T, P^T as bf16 over S^T, dv += P^T dout,
+//            dP^T = V dout^T, dS^T as bf16 over dP^T, dk += dS^T Q
+//
+// One tcgen05.mma issuer, two TMA issuers, eight warps for P and dS (warpgroup w takes the 64
+// columns [64 w, 64 w + 64) of each 128 x 128 tile, a thread one row).  Tensor memory, 512
+// columns: accumulator(s) 128 each, dq: two S buffers and one of dP; dk, dv: one of each.
+// The tile's MMAs run while the warps work on exponentials: dq issues dP of tile j + 1 and
+// S of tile j + 2 as soon as their buffers are read, dk of tile j and dP of tile j + 1 run
+// during the exponentials of tile j + 1.  An MMA that overwrites an operand of an earlier
+// one waits for that one's completion.
 // ---------------------------------------------------------------------------------
-struct BwdArgs {
-  const __nv_bfloat16 *q, *k_cur, *v_cur, *k_cache, *v_cache, *dout;
+constexpr int kBwdThreads = 352;     // 11 warps at up to 184 registers
+
+struct BwdParams {
+  // rows of H * d channels, boxes of 64 x 64: 2-D over the chunk's tokens, 3-D per frame
+  CUtensorMap q2, q3, g2, g3, kc2, kc3, vc2, vc3, kh, vh;
   __nv_bfloat16 *dq, *dk_cur, *dv_cur, *dk_cache, *dv_cache;
   const uint32_t* plan;
   const int32_t* plan_cnt;
@@ -232,130 +252,547 @@ struct BwdArgs {
   KeyTiles kt;
   const uint32_t* inv;
   const int32_t *inv_off, *inv_cnt;
+  int n_dq;                   // query tiles of all heads
+  uint64_t wait_limit_ns;
+  int debug_stall;            // test hook, as in the forward kernel
   int slots[LF_MAX_FRAMES];
 };
 
-template <int NC>
-__device__ __forceinline__ void row_load(const __nv_bfloat16* p, int lane, float* v) {
-#pragma unroll
-  for (int i = 0; i < NC / 2; ++i) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(p)[lane + 32 * i];
-    v[2 * i] = __uint_as_float(w << 16);
-    v[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-  }
-}
-
-template <int NC>
-__device__ __forceinline__ void row_store(__nv_bfloat16* p, int lane, const float* v) {
-#pragma unroll
-  for (int i = 0; i < NC / 2; ++i) {
-    __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    reinterpret_cast<uint32_t*>(p)[lane + 32 * i] = *reinterpret_cast<uint32_t*>(&t);
-  }
-}
-
-template <int NC>
-__device__ __forceinline__ float row_dot(const float* a, const float* b) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) s = fmaf(a[i], b[i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
+enum BwdBar {
+  kBbIn = 0, kBbS = 1, kBbDP = 3, kBbP = 4, kBbDS = 5, kBbAcc0 = 7, kBbAcc1 = 8, kBbDone = 9,
+  kBbRing0 = 10,               // full[3], empty[3]
+  kBbRing1 = 16,               // full[2], empty[2]
+  kBbCount = 20
+};
+constexpr int kRing0 = 3, kRing1 = 2;
 
 template <int HD>
-__global__ void __launch_bounds__(256) bwd_dq_simple_kernel(const __grid_constant__ BwdArgs A, const Dims D) {
-  constexpr int NC = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const int tok = blockIdx.x * 8 + (threadIdx.x >> 5), h = blockIdx.y;
-  if (tok >= D.ncur) return;
-  const float c = D.scale * 1.4426950408889634f;
-  const size_t row = ((size_t)tok * D.H + h) * HD;
-  float q[NC], g[NC], acc[NC] = {};
-  row_load<NC>(A.q + row, lane, q);
-  row_load<NC>(A.dout + row, lane, g);
-  const float nl = A.rows.dense_nlse[(size_t)h * bwd_dense_rows(D) + tok];
-  const float nd = A.rows.dense_nd[(size_t)h * bwd_dense_rows(D) + tok];
-  auto keys = [&](const __nv_bfloat16* kp, const __nv_bfloat16* vp, size_t first, int n) {
-    for (int i = 0; i < n; ++i) {
-      float k[NC], v[NC];
-      const size_t at = ((first + i) * D.H + h) * HD;
-      row_load<NC>(kp + at, lane, k);
-      row_load<NC>(vp + at, lane, v);
-      const float s = row_dot<NC>(q, k), dp = row_dot<NC>(g, v);
-      const float ds = exp2f(fmaf(s, c, nl)) * (dp + nd);
-      for (int j = 0; j < NC; ++j) acc[j] = fmaf(ds, k[j], acc[j]);
+struct BwdLayout {
+  static constexpr int NH = HD / 64;
+  static constexpr int kRegion = 128 * 128;            // 128 rows x 64 channels
+  static constexpr int kTile = NH * kRegion;
+  static constexpr int kMisc = kBbCount * 8;           // tensor-memory address, abort flag
+  static constexpr int kCols = 1024;                   // two tiles' boxes of row values
+  static constexpr int kIn0 = kCols + 2 * 2 * kBoxFloats * 4;
+  static constexpr int kIn1 = kIn0 + kTile;
+  static constexpr int kR0 = kIn1 + kTile;
+  static constexpr int kR1 = kR0 + kRing0 * kTile;
+  static constexpr int kBytes = kR1 + kRing1 * kTile;  // 227 KB at d = 128
+  static constexpr uint32_t kAcc0 = 0, kAcc1 = 128, kS1 = 128, kS0 = 256, kDP = 384;
+};
+static_assert(BwdLayout<128>::kIn0 % 1024 == 0 && BwdLayout<128>::kBytes <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// 64 rows x HD channels of one head into rows [64 box, 64 box + 64) of a tile: from a 2-D
+// map at `row`, or (frame >= 0) a 3-D one at frame and row.
+template <int HD>
+__device__ __forceinline__ void load_box(uint8_t* tile, int box, const CUtensorMap* m, uint64_t* bar,
+                                         int h, int row, int frame) {
+#pragma unroll
+  for (int c = 0; c < HD / 64; ++c) {
+    uint8_t* dst = tile + c * BwdLayout<HD>::kRegion + box * 64 * 128;
+    if (frame < 0) tma_load_2d(dst, m, bar, h * HD + c * 64, row);
+    else tma_load_3d(dst, m, bar, h * HD + c * 64, row, frame);
+  }
+}
+
+// D = A B^T over HD channels, both tiles K-major in shared memory.
+template <int HD>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
+#pragma unroll
+  for (int ks = 0; ks < HD / 16; ++ks) {
+    const uint32_t off = (ks >> 2) * BwdLayout<HD>::kRegion + (ks & 3) * 32;
+    mma_bf16_ss(d, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), idesc,
+                ks > 0 ? 1u : 0u);
+  }
+}
+
+// D (+)= A B over 128 columns of A: bf16 in tensor memory, columns [64 w, 64 w + 32) holding
+// the pairs of A's columns [64 w, 64 w + 64); B: 128 rows x HD in shared memory.
+template <int HD>
+__device__ __forceinline__ void mma_accumulate(uint32_t d, uint32_t a_tmem, uint32_t b, bool acc) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, HD, 0, 1);
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks)
+    mma_bf16_ts(d, a_tmem + (ks >> 2) * 64 + (ks & 3) * 8,
+                smem_desc_sw128(b + ks * 16 * 128, BwdLayout<HD>::kRegion, 1024), idesc,
+                acc || ks > 0 ? 1u : 0u);
+}
+
+// Two values rounded to bf16 and packed.
+__device__ __forceinline__ float pack_bf16(float a, float b) {
+  __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+  return __uint_as_float(*reinterpret_cast<uint32_t*>(&t));
+}
+
+// Warp w of the row warps hands its tensor-memory reads or writes to the MMA issuer.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// A row's HD accumulators from column `col` on, times f, as bf16 (zeros when !any).
+template <int N>
+__device__ __forceinline__ void store_row(uint32_t taddr, float f, bool any, bool store,
+                                          __nv_bfloat16* dst) {
+#pragma unroll
+  for (int ch = 0; ch < N / 32; ++ch) {
+    float v[32];
+    if (any) {
+      tmem_ld32(taddr + ch * 32, v);
+      tmem_ld_wait();
+      reg_fence32(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
     }
-  };
-  if (D.kc == 0) keys(A.k_cur, A.v_cur, 0, D.ncur);
-  const int qb = tok / D.T * D.nbpf + tok % D.T / D.B;
-  const int t = D.B == 64 ? qb / 2 : qb;
-  const uint32_t bit = D.B == 64 && (qb & 1) ? 2u : 1u;
-  const size_t tile = (size_t)h * tile_count(D) + t;
-  const int cnt = A.plan_cnt[tile];
-  for (int e = 0; e < cnt; ++e) {
-    const uint32_t pe = A.plan[tile * plan_stride(D) + e];
-    if (!(pe & bit)) continue;
-    const int p = (int)(pe >> 16), b = (int)((pe >> 4) & 0xFFFu);
-    if (p >= D.S + D.F)
-      keys(A.k_cur, A.v_cur, (size_t)(p - D.S - D.F) * D.T + b * D.B, block_len(D, b));
-    else
-      keys(A.k_cache, A.v_cache, (size_t)A.slots[p] * D.T + b * D.B, block_len(D, b));
-  }
-  for (int j = 0; j < NC; ++j) acc[j] *= D.scale;
-  row_store<NC>(A.dq + row, lane, acc);
-}
-
-template <int HD>
-__global__ void __launch_bounds__(256) bwd_dkv_simple_kernel(const __grid_constant__ BwdArgs A, const Dims D) {
-  constexpr int NC = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const KeyTile kt = key_tile_of(blockIdx.x, A.kt, D);
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);     // row of the tile
-  const int h = kt.h;
-  const int n_rows = kt.kind == 0 ? D.ncur : D.T;
-  if (kt.row + r >= n_rows) return;
-  const bool cur = kt.kind == 0 || kt.kind == 2;
-  const size_t tok = kt.kind == 0 ? (size_t)(kt.row + r)
-                     : (size_t)(kt.kind == 2   ? kt.frame
-                                : kt.kind == 1 ? A.slots[kt.frame]
-                                               : A.slots[D.S + kt.frame]) * D.T + kt.row + r;
-  const size_t row = (tok * D.H + h) * HD;
-  float k[NC], v[NC], dk[NC] = {}, dv[NC] = {};
-  row_load<NC>((cur ? A.k_cur : A.k_cache) + row, lane, k);
-  row_load<NC>((cur ? A.v_cur : A.v_cache) + row, lane, v);
-  const float c = D.scale * 1.4426950408889634f;
-  auto queries = [&](int first, int n, const float* nl, const float* nd) {
-    for (int i = 0; i < n; ++i) {
-      float q[NC], g[NC];
-      const size_t at = ((size_t)(first + i) * D.H + h) * HD;
-      row_load<NC>(A.q + at, lane, q);
-      row_load<NC>(A.dout + at, lane, g);
-      const float p = exp2f(fmaf(row_dot<NC>(q, k), c, nl[i]));
-      const float ds = p * (row_dot<NC>(g, v) + nd[i]);
-      for (int j = 0; j < NC; ++j) {
-        dv[j] = fmaf(p, g[j], dv[j]);
-        dk[j] = fmaf(ds, q[j], dk[j]);
+    if (store) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint4 w;
+        w.x = __float_as_uint(pack_bf16(v[8 * e] * f, v[8 * e + 1] * f));
+        w.y = __float_as_uint(pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f));
+        w.z = __float_as_uint(pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f));
+        w.w = __float_as_uint(pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f));
+        reinterpret_cast<uint4*>(dst)[ch * 4 + e] = w;
       }
     }
-  };
-  if (kt.list < 0) {
-    const size_t at = (size_t)h * bwd_dense_rows(D);
-    queries(0, D.ncur, A.rows.dense_nlse + at, A.rows.dense_nd + at);
+  }
+}
+
+template <int HD, int BLK>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
+  using L = BwdLayout<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = P.wait_limit_ns;
+
+  // ---- the CTA's tile and the number of tiles that it streams
+  const bool is_dq = (int)blockIdx.x < P.n_dq;
+  const int ntiles = tile_count(D);
+  const int n_dense = D.kc > 0 ? 0 : cdiv(D.ncur, 128);
+  int h, n_iter, cnt, qbA = 0, qbB = -1;
+  const uint32_t* entries;                          // key plan, or list of query blocks
+  KeyTile kt{};
+  int d0;                                           // tiles before this one are dense
+  if (is_dq) {
+    const int t = blockIdx.x % ntiles;
+    h = blockIdx.x / ntiles;
+    qbA = BLK == 64 ? 2 * t : t;
+    if (BLK == 64 && 2 * t + 1 < D.nqb) qbB = 2 * t + 1;
+    cnt = P.plan_cnt[blockIdx.x];
+    entries = P.plan + (size_t)blockIdx.x * plan_stride(D);
+    d0 = n_dense;
+    n_iter = d0 + (BLK == 64 ? cdiv(cnt, 2) : cnt);
   } else {
-    const uint32_t* list = A.inv + A.inv_off[kt.list];
-    for (int e = 0; e < A.inv_cnt[kt.list]; ++e) {
-      if (!(list[e] & (r < 64 ? 1u : 2u))) continue;
-      const int qb = (int)(list[e] >> 2);
-      const size_t at = (size_t)h * bwd_blk_rows(D) + (size_t)qb * D.B;
-      queries(qb / D.nbpf * D.T + qb % D.nbpf * D.B, block_len(D, qb % D.nbpf),
-              A.rows.blk_nlse + at, A.rows.blk_nd + at);
+    kt = key_tile_of(blockIdx.x - P.n_dq, P.kt, D);
+    h = kt.h;
+    if (kt.list < 0) {
+      cnt = 0;
+      entries = nullptr;
+      n_iter = d0 = cdiv(D.ncur, 128);
+    } else {
+      cnt = P.inv_cnt[kt.list];
+      entries = P.inv + P.inv_off[kt.list];
+      d0 = 0;
+      n_iter = BLK == 64 ? cdiv(cnt, 2) : cnt;
     }
   }
-  for (int j = 0; j < NC; ++j) dk[j] *= D.scale;
-  row_store<NC>((cur ? A.dk_cur : A.dk_cache) + row, lane, dk);
-  row_store<NC>((cur ? A.dv_cur : A.dv_cache) + row, lane, dv);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBbCount; ++i)
+      mbar_init(&bars[i], i == kBbP || i == kBbDS || i == kBbDS + 1 ? 8 : 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  uint8_t* in0 = smem + L::kIn0;
+  uint8_t* in1 = smem + L::kIn1;
+  // the window of dynamic shared memory starts on 1024 bytes (swizzled tiles need it)
+  const bool run = n_iter > 0 && (smem_u32(smem) & 1023u) == 0;
+  if (n_iter > 0 && !run && threadIdx.x == 0) record_status(LF_ERR_CUDA);
+
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ TMA issuers
+    if (lane == 0 && run) {
+      const bool side0 = warp == 0;                 // Q / K rings and inputs; else V, dout
+      const int n_slot = side0 ? kRing0 : kRing1;
+      uint64_t* full = &bars[side0 ? kBbRing0 : kBbRing1];
+      uint64_t* empty = full + n_slot;
+      uint8_t* ring = smem + (side0 ? L::kR0 : L::kR1);
+      // the CTA's own tiles, both on one barrier armed by warp 0
+      const bool stall = P.debug_stall && blockIdx.x == 0;
+      if (side0 && !stall) {
+        mbar_arrive_expect_tx(&bars[kBbIn], 2 * L::kTile);
+        for (int box = 0; box < 2; ++box) {
+          if (is_dq) {
+            const int qb = BLK == 64 ? (box ? qbB : qbA) : qbA;
+            const int f = qb >= 0 ? qb / D.nbpf : D.Fc;        // frame Fc reads as zeros
+            const int row = qb >= 0 ? (qb % D.nbpf) * BLK + (BLK == 128 ? box * 64 : 0) : 0;
+            load_box<HD>(in0, box, &P.q3, &bars[kBbIn], h, row, f);
+            load_box<HD>(in1, box, &P.g3, &bars[kBbIn], h, row, f);
+          } else {
+            const int row = kt.row + box * 64;
+            const bool dense = kt.kind == 0, cur = kt.kind == 2;
+            const int f = dense ? -1 : cur ? kt.frame
+                                           : P.slots[kt.kind == 1 ? kt.frame : D.S + kt.frame];
+            load_box<HD>(in0, box, dense ? &P.kc2 : cur ? &P.kc3 : &P.kh, &bars[kBbIn], h, row, f);
+            load_box<HD>(in1, box, dense ? &P.vc2 : cur ? &P.vc3 : &P.vh, &bars[kBbIn], h, row, f);
+          }
+        }
+      }
+      int j = 0;
+      for (; j < n_iter; ++j) {
+        const int slot = j % n_slot, rnd = j / n_slot;
+        if (rnd > 0 && !mbar_wait(&empty[slot], (rnd & 1) ^ 1, s_abort, limit)) break;
+        // the row values' buffer of tile j - 2 has been read
+        const bool cols = !is_dq && side0;
+        if (cols && j >= 2 && !mbar_wait(&bars[kBbDS + (j & 1)], ((j >> 1) & 1) ^ 1, s_abort, limit))
+          break;
+        mbar_arrive_expect_tx(&full[slot], L::kTile + (cols ? 2 * kBoxFloats * 4 : 0));
+        uint8_t* dst = ring + slot * L::kTile;
+        for (int box = 0; box < 2; ++box) {
+          if (is_dq) {
+            if (j < d0) {
+              load_box<HD>(dst, box, side0 ? &P.kc2 : &P.vc2, &full[slot], h, j * 128 + box * 64, -1);
+              continue;
+            }
+            const int e = BLK == 64 ? 2 * (j - d0) + box : j - d0;
+            int f = D.Fc, row = 0, p = D.S + D.F;              // past the plan's end: zeros
+            if (e < cnt) {
+              const uint32_t pe = entries[e];
+              p = (int)(pe >> 16);
+              row = (int)((pe >> 4) & 0xFFFu) * BLK + (BLK == 128 ? box * 64 : 0);
+              f = p < D.S + D.F ? P.slots[p] : p - (D.S + D.F);
+            }
+            if (p < D.S + D.F)
+              load_box<HD>(dst, box, side0 ? &P.kh : &P.vh, &full[slot], h, row, f);
+            else
+              load_box<HD>(dst, box, side0 ? &P.kc3 : &P.vc3, &full[slot], h, row, f);
+          } else {
+            const float* src;
+            if (j < d0) {
+              load_box<HD>(dst, box, side0 ? &P.q2 : &P.g2, &full[slot], h, j * 128 + box * 64, -1);
+              src = P.rows.dense + ((size_t)h * bwd_dense_boxes(D) + 2 * j + box) * kBoxFloats;
+            } else {
+              const int e = BLK == 64 ? 2 * j + box : j;
+              int f = D.Fc, row = 0;
+              size_t at = (size_t)D.H * bwd_blk_boxes(D);      // the box of padding
+              if (e < cnt) {
+                const int qb = (int)(entries[e] >> 2);
+                f = qb / D.nbpf;
+                row = (qb % D.nbpf) * BLK + (BLK == 128 ? box * 64 : 0);
+                at = (size_t)h * bwd_blk_boxes(D) + (BLK == 128 ? 2 * qb + box : qb);
+              }
+              load_box<HD>(dst, box, side0 ? &P.q3 : &P.g3, &full[slot], h, row, f);
+              src = P.rows.blk + at * kBoxFloats;
+            }
+            if (cols)
+              bulk_load(smem + L::kCols + ((j & 1) * 2 + box) * kBoxFloats * 4, src, kBoxFloats * 4,
+                        &full[slot]);
+          }
+        }
+      }
+      // every copy issued lands before the CTA may exit
+      if (side0 && !stall) mbar_wait_drain(&bars[kBbIn], 0, limit);
+      for (int x = max(0, j - n_slot); x < j; ++x)
+        mbar_wait_drain(&full[x % n_slot], (x / n_slot) & 1, limit);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t a0 = smem_u32(in0), a1 = smem_u32(in1);
+      const uint32_t r0 = smem_u32(smem + L::kR0), r1 = smem_u32(smem + L::kR1);
+      uint64_t* f0 = &bars[kBbRing0];
+      uint64_t* e0 = f0 + kRing0;
+      uint64_t* f1 = &bars[kBbRing1];
+      uint64_t* e1 = f1 + kRing1;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, s_abort, limit); };
+      auto ring0 = [&](int j) { return wait(&f0[j % kRing0], (j / kRing0) & 1); };
+      auto ring1 = [&](int j) { return wait(&f1[j % kRing1], (j / kRing1) & 1); };
+      auto slot0 = [&](int j) { return r0 + (j % kRing0) * L::kTile; };
+      auto slot1 = [&](int j) { return r1 + (j % kRing1) * L::kTile; };
+      bool ok = run && wait(&bars[kBbIn], 0);
+      if (is_dq) {
+        auto scores = [&](int j) {
+          mma_scores<HD>(tmem + (j & 1 ? L::kS1 : L::kS0), a0, slot0(j));
+          mma_commit(&bars[kBbS + (j & 1)]);
+        };
+        auto dprob = [&](int j) {
+          mma_scores<HD>(tmem + L::kDP, a1, slot1(j));
+          mma_commit(&bars[kBbDP]);
+          mma_commit(&e1[j % kRing1]);
+        };
+        if (ok && (ok = ring0(0))) scores(0);
+        if (ok && (ok = ring1(0))) dprob(0);
+        if (ok && n_iter > 1 && (ok = ring0(1))) scores(1);
+        for (int j = 0; ok && j < n_iter; ++j) {
+          if (j + 1 < n_iter) {                     // dP of the next tile, once this one's is read
+            ok = ring1(j + 1) && wait(&bars[kBbP], j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            dprob(j + 1);
+          }
+          ok = wait(&bars[kBbDS + (j & 1)], (j >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_accumulate<HD>(tmem + L::kAcc0, tmem + (j & 1 ? L::kS1 : L::kS0), slot0(j), j > 0);
+          mma_commit(&e0[j % kRing0]);
+          mma_commit(&bars[kBbAcc0]);
+          if (j + 2 < n_iter) {                     // S over dS of this tile, once it is consumed
+            ok = ring0(j + 2) && wait(&bars[kBbAcc0], j & 1);
+            if (!ok) break;
+            scores(j + 2);
+          }
+        }
+      } else {
+        auto scores = [&](int j) {
+          mma_scores<HD>(tmem + L::kS0, a0, slot0(j));
+          mma_commit(&bars[kBbS]);
+        };
+        auto dkey = [&](int j) {
+          if (!wait(&bars[kBbDS + (j & 1)], (j >> 1) & 1)) return false;
+          tc_fence_after();
+          mma_accumulate<HD>(tmem + L::kAcc0, tmem + L::kDP, slot0(j), j > 0);
+          mma_commit(&e0[j % kRing0]);
+          mma_commit(&bars[kBbAcc0]);
+          return true;
+        };
+        if (ok && (ok = ring0(0))) scores(0);
+        for (int j = 0; ok && j < n_iter; ++j) {
+          if (j > 0 && !(ok = dkey(j - 1))) break;
+          // dP over dS of the tile before, once it is consumed
+          ok = ring1(j) && (j == 0 || wait(&bars[kBbAcc0], (j - 1) & 1));
+          if (!ok) break;
+          mma_scores<HD>(tmem + L::kDP, a1, slot1(j));
+          mma_commit(&bars[kBbDP]);
+          ok = wait(&bars[kBbP], j & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_accumulate<HD>(tmem + L::kAcc1, tmem + L::kS0, slot1(j), j > 0);
+          mma_commit(&e1[j % kRing1]);
+          mma_commit(&bars[kBbAcc1]);
+          if (j + 1 < n_iter) {                     // S over P of this tile, once it is consumed
+            ok = ring0(j + 1) && wait(&bars[kBbAcc1], j & 1);
+            if (!ok) break;
+            scores(j + 1);
+          }
+        }
+        if (ok) dkey(n_iter - 1);
+      }
+      mma_commit(&bars[kBbDone]);
+    }
+  } else {
+    // ------------------------------------------------------------ P and dS
+    const int wg = (warp - 3) >> 2;                 // columns [64 wg, 64 wg + 64)
+    const int r = (warp & 3) * 32 + lane;           // row = tensor-memory lane
+    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const float c = D.scale * 1.4426950408889634f;
+    const float2 c2 = make_float2(c, c);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, s_abort, limit));
+    };
+    bool ok = run;
+    if (is_dq) {
+      const uint32_t bit = (BLK == 64 && r >= 64) ? 2u : 1u;
+      const int qb = BLK == 64 ? (r < 64 ? qbA : qbB) : qbA, i0 = BLK == 64 ? (r & 63) : r;
+      const bool valid = qb >= 0 && i0 < block_len(D, qb % D.nbpf);
+      const int tok = valid ? (qb / D.nbpf) * D.T + (qb % D.nbpf) * BLK + i0 : 0;
+      float nl = -INFINITY, nd = 0.f;
+      if (valid) {
+        const float* b = P.rows.dense + ((size_t)h * bwd_dense_boxes(D) + tok / 64) * kBoxFloats + tok % 64;
+        nl = b[0];
+        nd = b[64];
+      }
+      const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
+      // this tile's plan entry is read one tile ahead
+      auto entry = [&](int j) {
+        const int e = BLK == 64 ? 2 * (j - d0) + wg : j - d0;
+        return j >= d0 && j < n_iter && e < cnt ? entries[e] : 0u;
+      };
+      uint32_t pe = entry(0);
+      for (int j = 0; ok && j < n_iter; ++j) {
+        int v;                                      // valid key columns of this half
+        if (j < d0) {
+          v = max(0, min(64, D.ncur - j * 128 - wg * 64));
+        } else {
+          const int len = (pe & bit) ? block_len(D, (pe >> 4) & 0xFFF) : 0;
+          v = BLK == 64 ? len : max(0, min(64, len - wg * 64));
+        }
+        pe = entry(j + 1);
+        const uint32_t s_col = (j & 1 ? L::kS1 : L::kS0) + wg * 64;
+        if (!(ok = wait(&bars[kBbS + (j & 1)], (j >> 1) & 1))) break;
+        tc_fence_after();
+        float s[64];
+        if (v > 0) {
+          tmem_ld32(t_row + s_col, s);
+          tmem_ld32(t_row + s_col + 32, s + 32);
+          tmem_ld_wait();
+          reg_fence32(s);
+          reg_fence32(s + 32);
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            const float2 x = ffma2(make_float2(s[i], s[i + 1]), c2, nl2);
+            s[i] = ex2_approx(x.x);
+            s[i + 1] = ex2_approx(x.y);
+          }
+        }
+        if (!(ok = wait(&bars[kBbDP], j & 1))) break;
+        tc_fence_after();
+        if (v > 0) {
+          float g[64];
+          tmem_ld32(t_row + L::kDP + wg * 64, g);
+          tmem_ld32(t_row + L::kDP + wg * 64 + 32, g + 32);
+          tmem_ld_wait();
+          reg_fence32(g);
+          reg_fence32(g + 32);
+          warp_arrive(&bars[kBbP]);
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            const float2 x = fadd2(make_float2(g[i], g[i + 1]), nd2);
+            s[i] *= x.x;
+            s[i + 1] *= x.y;
+          }
+          if (v < 64) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= v) s[i] = 0.f;
+          }
+        } else {
+          warp_arrive(&bars[kBbP]);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) s[i] = 0.f;
+        }
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          float pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(s[ch * 32 + 2 * e], s[ch * 32 + 2 * e + 1]);
+          tmem_st16(t_row + s_col + ch * 16, pk);
+        }
+        tmem_st_wait();
+        warp_arrive(&bars[kBbDS + (j & 1)]);
+      }
+      const bool done = wait(&bars[kBbDone], 0);
+      tc_fence_after();
+      if ((ok || n_iter == 0) && done)
+        store_row<HD / 2>(t_row + L::kAcc0 + wg * (HD / 2), D.scale, n_iter > 0, valid,
+                          P.dq + ((size_t)tok * D.H + h) * HD + wg * (HD / 2));
+    } else {
+      const uint32_t bit = r < 64 ? 1u : 2u;
+      auto entry = [&](int j) {                     // dense: every row attends
+        const int e = BLK == 64 ? 2 * j + wg : j;
+        return j < d0 ? 3u : j < n_iter && e < cnt ? entries[e] : 0u;
+      };
+      uint32_t pe = entry(0);
+      for (int j = 0; ok && j < n_iter; ++j) {
+        const bool on = (pe & bit) != 0;
+        pe = entry(j + 1);
+        const float4* nl4 = reinterpret_cast<const float4*>(
+            smem + L::kCols + ((j & 1) * 2 + wg) * kBoxFloats * 4);
+        if (!(ok = wait(&bars[kBbS], j & 1))) break;
+        tc_fence_after();
+        float s[64];
+        // the row values came with the ring slot that S was computed from; the issuer of S
+        // has waited for it, this thread has to as well (asynchronous copies)
+        if (!(ok = wait(&bars[kBbRing0 + j % kRing0], (j / kRing0) & 1))) break;
+        if (on) {
+          tmem_ld32(t_row + L::kS0 + wg * 64, s);
+          tmem_ld32(t_row + L::kS0 + wg * 64 + 32, s + 32);
+          tmem_ld_wait();
+          reg_fence32(s);
+          reg_fence32(s + 32);
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const float4 n = nl4[i / 4];
+            const float2 x = ffma2(make_float2(s[i], s[i + 1]), c2, make_float2(n.x, n.y));
+            const float2 y = ffma2(make_float2(s[i + 2], s[i + 3]), c2, make_float2(n.z, n.w));
+            s[i] = ex2_approx(x.x);
+            s[i + 1] = ex2_approx(x.y);
+            s[i + 2] = ex2_approx(y.x);
+            s[i + 3] = ex2_approx(y.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) s[i] = 0.f;
+        }
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          float pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(s[ch * 32 + 2 * e], s[ch * 32 + 2 * e + 1]);
+          tmem_st16(t_row + L::kS0 + wg * 64 + ch * 16, pk);
+        }
+        tmem_st_wait();
+        warp_arrive(&bars[kBbP]);
+        if (!(ok = wait(&bars[kBbDP], j & 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          float pk[16];
+          if (on) {
+            float g[32];
+            tmem_ld32(t_row + L::kDP + wg * 64 + ch * 32, g);
+            tmem_ld_wait();
+            reg_fence32(g);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 n = nl4[16 + ch * 8 + i / 4];
+              const float2 x = fadd2(make_float2(g[i], g[i + 1]), make_float2(n.x, n.y));
+              const float2 y = fadd2(make_float2(g[i + 2], g[i + 3]), make_float2(n.z, n.w));
+              const float* p = s + ch * 32 + i;
+              pk[i / 2] = pack_bf16(p[0] * x.x, p[1] * x.y);
+              pk[i / 2 + 1] = pack_bf16(p[2] * y.x, p[3] * y.y);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 0.f;
+          }
+          tmem_st16(t_row + L::kDP + wg * 64 + ch * 16, pk);
+        }
+        tmem_st_wait();
+        warp_arrive(&bars[kBbDS + (j & 1)]);
+      }
+      const bool done = wait(&bars[kBbDone], 0);
+      tc_fence_after();
+      if ((ok || n_iter == 0) && done) {
+        const bool cur = kt.kind == 0 || kt.kind == 2;
+        const bool valid = kt.row + r < (kt.kind == 0 ? D.ncur : D.T);
+        const size_t tok = (size_t)kt.row + r + (kt.kind == 0 ? 0
+                           : (size_t)(kt.kind == 2 ? kt.frame
+                                      : P.slots[kt.kind == 1 ? kt.frame : D.S + kt.frame]) * D.T);
+        __nv_bfloat16* dst = wg == 0 ? (cur ? P.dk_cur : P.dk_cache) : (cur ? P.dv_cur : P.dv_cache);
+        store_row<HD>(t_row + (wg == 0 ? L::kAcc0 : L::kAcc1), wg == 0 ? D.scale : 1.f, n_iter > 0,
+                      valid, dst + (tok * D.H + h) * HD);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) mbar_wait_drain(&bars[kBbDone], 0, limit);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 }  // namespace lf
