@@ -91,14 +91,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // bf16 rows of H*d channels: 2-D [rows, H*d] or 3-D [slots, T, H*d]; box = 64 channels x
-// 64 rows (x 1 slot); 128-byte swizzle; out-of-bounds elements read as zero.
-int encode_rows(CUtensorMap* m, const void* base, int HD, long long rows, int slots) {
+// 64 (or box_rows) rows (x 1 slot); 128-byte swizzle; out-of-bounds elements read as zero.
+int encode_rows(CUtensorMap* m, const void* base, int HD, long long rows, int slots,
+                int box_rows = 64) {
   auto fn = encode_fn();
   if (fn == nullptr) return LF_ERR_CUDA;
   const cuuint32_t rank = slots > 0 ? 3 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)HD, (cuuint64_t)rows, (cuuint64_t)(slots > 0 ? slots : 1)};
   cuuint64_t strides[2] = {(cuuint64_t)HD * 2, (cuuint64_t)HD * 2 * (cuuint64_t)rows};
-  cuuint32_t box[3] = {64, 64, 1};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims,
                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -513,6 +514,10 @@ int launch_bwd_t(const Dims& D, const lf::BwdParams& p, int grid, cudaStream_t s
   constexpr int smem = lf::BwdLayout<HD>::kBytes;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return LF_ERR_CUDA;
+  // the in-kernel register split assumes the launch register count; never launch otherwise
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return LF_ERR_CUDA;
+  if (fa.numRegs != lf::kBwdLaunchRegs) return LF_ERR_UNSUPPORTED;
   kern<<<grid, lf::kBwdThreads, smem, st>>>(p, D);
   return cuda_status(cudaGetLastError());
 }
@@ -546,7 +551,7 @@ int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
   const struct { CUtensorMap *m2, *m3; const void* base; } chunk[4] = {
       {&p.q2, &p.q3, b.q}, {&p.g2, &p.g3, b.dout}, {&p.kc2, &p.kc3, b.k_cur}, {&p.vc2, &p.vc3, b.v_cur}};
   for (const auto& m : chunk) {
-    if ((rc = encode_rows(m.m2, m.base, HD, D.ncur, 0)) != LF_OK) return rc;
+    if ((rc = encode_rows(m.m2, m.base, HD, D.ncur, 0, 128)) != LF_OK) return rc;
     if ((rc = encode_rows(m.m3, m.base, HD, D.T, D.Fc)) != LF_OK) return rc;
   }
   if (D.F + D.S > 0) {

@@ -230,20 +230,33 @@ bwd_transpose_kernel(const uint32_t* __restrict__ plan, const int32_t* __restric
 //
 //   dq:      S = Q K^T, dP = dout V^T, dS = P (dP - D) as bf16 over S, dq += dS K
 //   dk, dv:  S^T = K Q^T, P^T as bf16 over S^T, dv += P^T dout,
-//            dP^T = V dout^T, dS^T as bf16 over dP^T, dk += dS^T Q
+//            dP^T = V dout^T, dS^T as bf16 beside P^T, dk += dS^T Q
 //
-// One tcgen05.mma issuer, two TMA issuers, eight warps for P and dS (warpgroup w takes the 64
-// columns [64 w, 64 w + 64) of each 128 x 128 tile, a thread one row).  Tensor memory, 512
-// columns: accumulator(s) 128 each, dq: two S buffers and one of dP; dk, dv: one of each.
-// The tile's MMAs run while the warps work on exponentials: dq issues dP of tile j + 1 and
-// S of tile j + 2 as soon as their buffers are read, dk of tile j and dP of tile j + 1 run
-// during the exponentials of tile j + 1.  An MMA that overwrites an operand of an earlier
-// one waits for that one's completion.
+// Four warps issue (two TMA, two tcgen05.mma: scores and dP by one, the accumulating products
+// by the other, so that neither waits behind the other's operands), eight make P and dS.
+// Tensor memory has 512 columns; the accumulators take 128 (dq) or 256 (dk and dv).
+//
+//   dq: buffers S0, S1 and one of dP.  Warpgroup w takes tiles w, w + 2, ... whole, a thread
+//   one row of 128 columns: while one warpgroup is at the exponentials of its tile (1024 clk
+//   of the special-function units), the other multiplies and stores dS of its own.
+//   dk, dv: buffers X0, X1.  Tile j has S in X[j & 1] and dP in the other one, P and dS both
+//   go over S, so dP's buffer is free for the next tile's S once it has been read, and the
+//   exponentials of tile j + 1 overlap dk of tile j and dP of tile j + 1.  Warpgroup w takes
+//   columns [64 w, 64 w + 64) of every tile.
+//
+// A barrier that is waited for every other tile, or whose next completion does not depend on
+// the waiting thread, exists twice, one for even and one for odd tiles: a wait on a parity
+// sees at most one completion ahead.  An MMA that overwrites an operand of an earlier one
+// waits for that one's completion.
 // ---------------------------------------------------------------------------------
-constexpr int kBwdThreads = 352;     // 11 warps at up to 184 registers
+constexpr int kBwdThreads = 384;
+// Register split, as in the forward kernel: 128 x 72 + 256 x 216 = 384 x 168.
+constexpr int kBwdLaunchRegs = 168, kBwdLowRegs = 72, kBwdHighRegs = 216;
+static_assert(128 * kBwdLowRegs + 256 * kBwdHighRegs <= kBwdThreads * kBwdLaunchRegs, "register split");
 
 struct BwdParams {
-  // rows of H * d channels, boxes of 64 x 64: 2-D over the chunk's tokens, 3-D per frame
+  // rows of H * d channels: 2-D over the chunk's tokens, boxes of 64 channels x 128 rows, and
+  // 3-D per frame, boxes of 64 x 64
   CUtensorMap q2, q3, g2, g3, kc2, kc3, vc2, vc3, kh, vh;
   __nv_bfloat16 *dq, *dk_cur, *dv_cur, *dk_cache, *dv_cache;
   const uint32_t* plan;
@@ -259,10 +272,17 @@ struct BwdParams {
 };
 
 enum BwdBar {
-  kBbIn = 0, kBbS = 1, kBbDP = 3, kBbP = 4, kBbDS = 5, kBbAcc0 = 7, kBbAcc1 = 8, kBbDone = 9,
-  kBbRing0 = 10,               // full[3], empty[3]
-  kBbRing1 = 16,               // full[2], empty[2]
-  kBbCount = 20
+  kBbIn = 0,                   // the CTA's own tiles
+  kBbS = 1,                    // [2] S of a tile
+  kBbDP = 3,                   // [2] dP of a tile
+  kBbP = 5,                    // [2] P written (dk, dv)
+  kBbRd = 7,                   // dP read
+  kBbDS = 8,                   // [2] dS written
+  kBbAcc = 10,                 // [2] accumulating products of a tile complete
+  kBbDone = 12,                // everything issued is complete (two issuers)
+  kBbRing0 = 13,               // full[3], empty[3]
+  kBbRing1 = 19,               // full[2], empty[2]
+  kBbCount = 23
 };
 constexpr int kRing0 = 3, kRing1 = 2;
 
@@ -278,51 +298,113 @@ struct BwdLayout {
   static constexpr int kR0 = kIn1 + kTile;
   static constexpr int kR1 = kR0 + kRing0 * kTile;
   static constexpr int kBytes = kR1 + kRing1 * kTile;  // 227 KB at d = 128
-  static constexpr uint32_t kAcc0 = 0, kAcc1 = 128, kS1 = 128, kS0 = 256, kDP = 384;
+  static constexpr uint32_t kAcc0 = 0, kAcc1 = 128;    // dq or dk; dv
+  static constexpr uint32_t kX0 = 256, kX1 = 384;      // dk, dv
+  static constexpr uint32_t kS0 = 128, kS1 = 256, kDP = 384;   // dq
 };
 static_assert(BwdLayout<128>::kIn0 % 1024 == 0 && BwdLayout<128>::kBytes <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-      ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+// Tensor-core and copy instructions of one elected lane, issued from code that the whole warp
+// runs: their operands (descriptors, addresses) then stay in uniform registers.  Issued from
+// a lane-0 branch, 8 MMAs took the issuer 850-1100 clk instead of the 560 that they run.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return r;
 }
 
-// 64 rows x HD channels of one head into rows [64 box, 64 box + 64) of a tile: from a 2-D
-// map at `row`, or (frame >= 0) a 3-D one at frame and row.
+__device__ __forceinline__ void mma_ss_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead) : "memory");
+}
+
+__device__ __forceinline__ void mma_ts_if(uint32_t lead, uint32_t d, uint32_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead) : "memory");
+}
+
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(lead) : "memory");
+}
+
+__device__ __forceinline__ void expect_if(uint32_t lead, uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b64 st;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
+      ::"r"(smem_u32(bar)), "r"(bytes), "r"(lead) : "memory");
+}
+
+__device__ __forceinline__ void bulk_load_if(uint32_t lead, void* dst, const void* src,
+                                             uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+      "@q cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}"
+      ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "r"(lead) : "memory");
+}
+
+// 128 rows x HD channels of one head from a 2-D map at `row`.
 template <int HD>
-__device__ __forceinline__ void load_box(uint8_t* tile, int box, const CUtensorMap* m, uint64_t* bar,
-                                         int h, int row, int frame) {
+__device__ __forceinline__ void load_tile_if(uint32_t lead, uint8_t* tile, const CUtensorMap* m,
+                                             uint64_t* bar, int h, int row) {
 #pragma unroll
-  for (int c = 0; c < HD / 64; ++c) {
-    uint8_t* dst = tile + c * BwdLayout<HD>::kRegion + box * 64 * 128;
-    if (frame < 0) tma_load_2d(dst, m, bar, h * HD + c * 64, row);
-    else tma_load_3d(dst, m, bar, h * HD + c * 64, row, frame);
-  }
+  for (int c = 0; c < HD / 64; ++c)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];\n\t}"
+        ::"r"(smem_u32(tile + c * BwdLayout<HD>::kRegion)), "l"(m), "r"(smem_u32(bar)),
+          "r"(h * HD + c * 64), "r"(row), "r"(lead) : "memory");
+}
+
+// 64 rows x HD channels of one head into rows [64 box, 64 box + 64) of a tile, from a 3-D map
+// at frame and row; rows past the frame's end, and frames past the last, read as zeros.
+template <int HD>
+__device__ __forceinline__ void load_box_if(uint32_t lead, uint8_t* tile, int box,
+                                            const CUtensorMap* m, uint64_t* bar, int h, int row,
+                                            int frame) {
+#pragma unroll
+  for (int c = 0; c < HD / 64; ++c)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}"
+        ::"r"(smem_u32(tile + c * BwdLayout<HD>::kRegion + box * 64 * 128)), "l"(m),
+          "r"(smem_u32(bar)), "r"(h * HD + c * 64), "r"(row), "r"(frame), "r"(lead) : "memory");
 }
 
 // D = A B^T over HD channels, both tiles K-major in shared memory.
 template <int HD>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void mma_scores(uint32_t lead, uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
+  const uint64_t da = smem_desc_sw128(a, 16, 1024), db = smem_desc_sw128(b, 16, 1024);
 #pragma unroll
   for (int ks = 0; ks < HD / 16; ++ks) {
-    const uint32_t off = (ks >> 2) * BwdLayout<HD>::kRegion + (ks & 3) * 32;
-    mma_bf16_ss(d, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), idesc,
-                ks > 0 ? 1u : 0u);
+    const uint64_t off = ((ks >> 2) * BwdLayout<HD>::kRegion + (ks & 3) * 32) >> 4;
+    mma_ss_if(lead, d, da + off, db + off, idesc, ks > 0 ? 1u : 0u);
   }
 }
 
-// D (+)= A B over 128 columns of A: bf16 in tensor memory, columns [64 w, 64 w + 32) holding
-// the pairs of A's columns [64 w, 64 w + 64); B: 128 rows x HD in shared memory.
+// D (+)= A B over 128 columns of A: bf16 pairs in tensor memory, `half` columns between the
+// pairs of A's first and last 64 columns; B: 128 rows x HD in shared memory.
 template <int HD>
-__device__ __forceinline__ void mma_accumulate(uint32_t d, uint32_t a_tmem, uint32_t b, bool acc) {
+__device__ __forceinline__ void mma_accumulate(uint32_t lead, uint32_t d, uint32_t a_tmem, int half,
+                                               uint32_t b, bool acc) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, HD, 0, 1);
+  const uint64_t db = smem_desc_sw128(b, BwdLayout<HD>::kRegion, 1024);
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks)
-    mma_bf16_ts(d, a_tmem + (ks >> 2) * 64 + (ks & 3) * 8,
-                smem_desc_sw128(b + ks * 16 * 128, BwdLayout<HD>::kRegion, 1024), idesc,
-                acc || ks > 0 ? 1u : 0u);
+    mma_ts_if(lead, d, a_tmem + (ks >> 2) * half + (ks & 3) * 8, db + (ks * 16 * 128 >> 4), idesc,
+              acc || ks > 0 ? 1u : 0u);
 }
 
 // Two values rounded to bf16 and packed.
@@ -331,14 +413,14 @@ __device__ __forceinline__ float pack_bf16(float a, float b) {
   return __uint_as_float(*reinterpret_cast<uint32_t*>(&t));
 }
 
-// Warp w of the row warps hands its tensor-memory reads or writes to the MMA issuer.
+// A row warp hands its tensor-memory reads or writes to the MMA issuers.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   tc_fence_before();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// A row's HD accumulators from column `col` on, times f, as bf16 (zeros when !any).
+// N accumulators of a row, times f, as bf16 (zeros when !any).
 template <int N>
 __device__ __forceinline__ void store_row(uint32_t taddr, float f, bool any, bool store,
                                           __nv_bfloat16* dst) {
@@ -411,8 +493,10 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
   }
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kBbCount; ++i)
-      mbar_init(&bars[i], i == kBbP || i == kBbDS || i == kBbDS + 1 ? 8 : 1);
+    for (int i = 0; i < kBbCount; ++i) {
+      const bool rows = i == kBbP || i == kBbP + 1 || i == kBbRd || i == kBbDS || i == kBbDS + 1;
+      mbar_init(&bars[i], rows ? (is_dq ? 4 : 8) : i == kBbDone ? 2 : 1);
+    }
     *s_abort = 0;
     fence_mbar_init();
   }
@@ -423,193 +507,201 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  constexpr uint32_t tmem = 0;        // all 512 columns are this CTA's: they start at 0
   uint8_t* in0 = smem + L::kIn0;
   uint8_t* in1 = smem + L::kIn1;
   // the window of dynamic shared memory starts on 1024 bytes (swizzled tiles need it)
   const bool run = n_iter > 0 && (smem_u32(smem) & 1023u) == 0;
   if (n_iter > 0 && !run && threadIdx.x == 0) record_status(LF_ERR_CUDA);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, s_abort, limit)) != 0;
+  };
 
-  if (warp == 0 || warp == 2) {
-    // ------------------------------------------------------------ TMA issuers
-    if (lane == 0 && run) {
-      const bool side0 = warp == 0;                 // Q / K rings and inputs; else V, dout
+  if (warp < 4) {
+    regs_dec<kBwdLowRegs>();
+    const uint32_t lead = elect_lane();
+    if (warp == 0 || warp == 2) {
+      // ---------------------------------------------------------- TMA issuers
+      const bool side0 = warp == 0;                 // Q / K ring and both inputs; else V / dout
       const int n_slot = side0 ? kRing0 : kRing1;
       uint64_t* full = &bars[side0 ? kBbRing0 : kBbRing1];
       uint64_t* empty = full + n_slot;
       uint8_t* ring = smem + (side0 ? L::kR0 : L::kR1);
-      // the CTA's own tiles, both on one barrier armed by warp 0
       const bool stall = P.debug_stall && blockIdx.x == 0;
-      if (side0 && !stall) {
-        mbar_arrive_expect_tx(&bars[kBbIn], 2 * L::kTile);
-        for (int box = 0; box < 2; ++box) {
-          if (is_dq) {
-            const int qb = BLK == 64 ? (box ? qbB : qbA) : qbA;
-            const int f = qb >= 0 ? qb / D.nbpf : D.Fc;        // frame Fc reads as zeros
-            const int row = qb >= 0 ? (qb % D.nbpf) * BLK + (BLK == 128 ? box * 64 : 0) : 0;
-            load_box<HD>(in0, box, &P.q3, &bars[kBbIn], h, row, f);
-            load_box<HD>(in1, box, &P.g3, &bars[kBbIn], h, row, f);
-          } else {
-            const int row = kt.row + box * 64;
-            const bool dense = kt.kind == 0, cur = kt.kind == 2;
-            const int f = dense ? -1 : cur ? kt.frame
-                                           : P.slots[kt.kind == 1 ? kt.frame : D.S + kt.frame];
-            load_box<HD>(in0, box, dense ? &P.kc2 : cur ? &P.kc3 : &P.kh, &bars[kBbIn], h, row, f);
-            load_box<HD>(in1, box, dense ? &P.vc2 : cur ? &P.vc3 : &P.vh, &bars[kBbIn], h, row, f);
+      if (side0 && run && !stall) {
+        expect_if(lead, &bars[kBbIn], 2 * L::kTile);
+        if (!is_dq && kt.kind == 0) {
+          load_tile_if<HD>(lead, in0, &P.kc2, &bars[kBbIn], h, kt.row);
+          load_tile_if<HD>(lead, in1, &P.vc2, &bars[kBbIn], h, kt.row);
+        } else {
+          for (int box = 0; box < 2; ++box) {
+            int f, row;
+            if (is_dq) {
+              const int qb = BLK == 64 && box ? qbB : qbA;
+              f = qb >= 0 ? qb / D.nbpf : D.Fc;                // frame Fc reads as zeros
+              row = qb >= 0 ? (qb % D.nbpf) * BLK + (BLK == 128 ? box * 64 : 0) : 0;
+            } else {
+              f = kt.kind == 2 ? kt.frame : P.slots[kt.kind == 1 ? kt.frame : D.S + kt.frame];
+              row = kt.row + box * 64;
+            }
+            load_box_if<HD>(lead, in0, box, is_dq ? &P.q3 : kt.kind == 2 ? &P.kc3 : &P.kh,
+                            &bars[kBbIn], h, row, f);
+            load_box_if<HD>(lead, in1, box, is_dq ? &P.g3 : kt.kind == 2 ? &P.vc3 : &P.vh,
+                            &bars[kBbIn], h, row, f);
           }
         }
       }
-      int j = 0;
-      for (; j < n_iter; ++j) {
-        const int slot = j % n_slot, rnd = j / n_slot;
-        if (rnd > 0 && !mbar_wait(&empty[slot], (rnd & 1) ^ 1, s_abort, limit)) break;
+      int j = 0, slot = 0, rnd = 0;
+      for (; run && j < n_iter; ++j) {
+        if (rnd > 0 && !wait(&empty[slot], (rnd & 1) ^ 1)) break;
         // the row values' buffer of tile j - 2 has been read
         const bool cols = !is_dq && side0;
-        if (cols && j >= 2 && !mbar_wait(&bars[kBbDS + (j & 1)], ((j >> 1) & 1) ^ 1, s_abort, limit))
-          break;
-        mbar_arrive_expect_tx(&full[slot], L::kTile + (cols ? 2 * kBoxFloats * 4 : 0));
+        if (cols && j >= 2 && !wait(&bars[kBbDS + (j & 1)], ((j >> 1) & 1) ^ 1)) break;
+        expect_if(lead, &full[slot], L::kTile + (cols ? 2 * kBoxFloats * 4 : 0));
         uint8_t* dst = ring + slot * L::kTile;
-        for (int box = 0; box < 2; ++box) {
+        float* col = reinterpret_cast<float*>(smem + L::kCols) + (j & 1) * 2 * kBoxFloats;
+        if (j < d0) {
           if (is_dq) {
-            if (j < d0) {
-              load_box<HD>(dst, box, side0 ? &P.kc2 : &P.vc2, &full[slot], h, j * 128 + box * 64, -1);
-              continue;
-            }
-            const int e = BLK == 64 ? 2 * (j - d0) + box : j - d0;
-            int f = D.Fc, row = 0, p = D.S + D.F;              // past the plan's end: zeros
-            if (e < cnt) {
-              const uint32_t pe = entries[e];
-              p = (int)(pe >> 16);
-              row = (int)((pe >> 4) & 0xFFFu) * BLK + (BLK == 128 ? box * 64 : 0);
-              f = p < D.S + D.F ? P.slots[p] : p - (D.S + D.F);
-            }
-            if (p < D.S + D.F)
-              load_box<HD>(dst, box, side0 ? &P.kh : &P.vh, &full[slot], h, row, f);
-            else
-              load_box<HD>(dst, box, side0 ? &P.kc3 : &P.vc3, &full[slot], h, row, f);
+            load_tile_if<HD>(lead, dst, side0 ? &P.kc2 : &P.vc2, &full[slot], h, j * 128);
           } else {
-            const float* src;
-            if (j < d0) {
-              load_box<HD>(dst, box, side0 ? &P.q2 : &P.g2, &full[slot], h, j * 128 + box * 64, -1);
-              src = P.rows.dense + ((size_t)h * bwd_dense_boxes(D) + 2 * j + box) * kBoxFloats;
+            load_tile_if<HD>(lead, dst, side0 ? &P.q2 : &P.g2, &full[slot], h, j * 128);
+            if (cols)
+              bulk_load_if(lead, col,
+                           P.rows.dense + ((size_t)h * bwd_dense_boxes(D) + 2 * j) * kBoxFloats,
+                           2 * kBoxFloats * 4, &full[slot]);
+          }
+        } else {
+          for (int box = 0; box < 2; ++box) {
+            const int e = BLK == 64 ? 2 * (j - d0) + box : j - d0;
+            const uint32_t pe = e < cnt ? entries[e] : 0u;
+            int f = D.Fc, row = 0;                             // past the end: zeros
+            if (is_dq) {
+              bool cached = false;
+              if (e < cnt) {
+                const int p = (int)(pe >> 16);
+                row = (int)((pe >> 4) & 0xFFFu) * BLK + (BLK == 128 ? box * 64 : 0);
+                cached = p < D.S + D.F;
+                f = cached ? P.slots[p] : p - (D.S + D.F);
+              }
+              load_box_if<HD>(lead, dst, box,
+                              cached ? (side0 ? &P.kh : &P.vh) : (side0 ? &P.kc3 : &P.vc3),
+                              &full[slot], h, row, f);
             } else {
-              const int e = BLK == 64 ? 2 * j + box : j;
-              int f = D.Fc, row = 0;
               size_t at = (size_t)D.H * bwd_blk_boxes(D);      // the box of padding
               if (e < cnt) {
-                const int qb = (int)(entries[e] >> 2);
+                const int qb = (int)(pe >> 2);
                 f = qb / D.nbpf;
                 row = (qb % D.nbpf) * BLK + (BLK == 128 ? box * 64 : 0);
                 at = (size_t)h * bwd_blk_boxes(D) + (BLK == 128 ? 2 * qb + box : qb);
               }
-              load_box<HD>(dst, box, side0 ? &P.q3 : &P.g3, &full[slot], h, row, f);
-              src = P.rows.blk + at * kBoxFloats;
+              load_box_if<HD>(lead, dst, box, side0 ? &P.q3 : &P.g3, &full[slot], h, row, f);
+              if (cols)
+                bulk_load_if(lead, col + box * kBoxFloats, P.rows.blk + at * kBoxFloats,
+                             kBoxFloats * 4, &full[slot]);
             }
-            if (cols)
-              bulk_load(smem + L::kCols + ((j & 1) * 2 + box) * kBoxFloats * 4, src, kBoxFloats * 4,
-                        &full[slot]);
           }
         }
+        if (++slot == n_slot) { slot = 0; ++rnd; }
       }
       // every copy issued lands before the CTA may exit
-      if (side0 && !stall) mbar_wait_drain(&bars[kBbIn], 0, limit);
+      if (run && side0 && !stall) mbar_wait_drain(&bars[kBbIn], 0, limit);
       for (int x = max(0, j - n_slot); x < j; ++x)
         mbar_wait_drain(&full[x % n_slot], (x / n_slot) & 1, limit);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    } else {
+      // ---------------------------------------------------------- MMA issuers
       const uint32_t a0 = smem_u32(in0), a1 = smem_u32(in1);
       const uint32_t r0 = smem_u32(smem + L::kR0), r1 = smem_u32(smem + L::kR1);
       uint64_t* f0 = &bars[kBbRing0];
       uint64_t* e0 = f0 + kRing0;
       uint64_t* f1 = &bars[kBbRing1];
       uint64_t* e1 = f1 + kRing1;
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, s_abort, limit); };
       auto ring0 = [&](int j) { return wait(&f0[j % kRing0], (j / kRing0) & 1); };
       auto ring1 = [&](int j) { return wait(&f1[j % kRing1], (j / kRing1) & 1); };
       auto slot0 = [&](int j) { return r0 + (j % kRing0) * L::kTile; };
       auto slot1 = [&](int j) { return r1 + (j % kRing1) * L::kTile; };
       bool ok = run && wait(&bars[kBbIn], 0);
-      if (is_dq) {
+      if (warp == 1 && is_dq) {
         auto scores = [&](int j) {
-          mma_scores<HD>(tmem + (j & 1 ? L::kS1 : L::kS0), a0, slot0(j));
-          mma_commit(&bars[kBbS + (j & 1)]);
+          mma_scores<HD>(lead, tmem + (j & 1 ? L::kS1 : L::kS0), a0, slot0(j));
+          commit_if(lead, &bars[kBbS + (j & 1)]);
         };
         auto dprob = [&](int j) {
-          mma_scores<HD>(tmem + L::kDP, a1, slot1(j));
-          mma_commit(&bars[kBbDP]);
-          mma_commit(&e1[j % kRing1]);
+          mma_scores<HD>(lead, tmem + L::kDP, a1, slot1(j));
+          commit_if(lead, &bars[kBbDP + (j & 1)]);
+          commit_if(lead, &e1[j % kRing1]);
         };
         if (ok && (ok = ring0(0))) scores(0);
-        if (ok && (ok = ring1(0))) dprob(0);
         if (ok && n_iter > 1 && (ok = ring0(1))) scores(1);
+        if (ok && (ok = ring1(0))) dprob(0);
         for (int j = 0; ok && j < n_iter; ++j) {
           if (j + 1 < n_iter) {                     // dP of the next tile, once this one's is read
-            ok = ring1(j + 1) && wait(&bars[kBbP], j & 1);
+            ok = ring1(j + 1) && wait(&bars[kBbRd], j & 1);
             if (!ok) break;
             tc_fence_after();
             dprob(j + 1);
           }
-          ok = wait(&bars[kBbDS + (j & 1)], (j >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          mma_accumulate<HD>(tmem + L::kAcc0, tmem + (j & 1 ? L::kS1 : L::kS0), slot0(j), j > 0);
-          mma_commit(&e0[j % kRing0]);
-          mma_commit(&bars[kBbAcc0]);
           if (j + 2 < n_iter) {                     // S over dS of this tile, once it is consumed
-            ok = ring0(j + 2) && wait(&bars[kBbAcc0], j & 1);
+            ok = ring0(j + 2) && wait(&bars[kBbAcc + (j & 1)], (j >> 1) & 1);
             if (!ok) break;
+            tc_fence_after();
             scores(j + 2);
           }
         }
-      } else {
+      } else if (warp == 1) {
         auto scores = [&](int j) {
-          mma_scores<HD>(tmem + L::kS0, a0, slot0(j));
-          mma_commit(&bars[kBbS]);
-        };
-        auto dkey = [&](int j) {
-          if (!wait(&bars[kBbDS + (j & 1)], (j >> 1) & 1)) return false;
-          tc_fence_after();
-          mma_accumulate<HD>(tmem + L::kAcc0, tmem + L::kDP, slot0(j), j > 0);
-          mma_commit(&e0[j % kRing0]);
-          mma_commit(&bars[kBbAcc0]);
-          return true;
+          mma_scores<HD>(lead, tmem + (j & 1 ? L::kX1 : L::kX0), a0, slot0(j));
+          commit_if(lead, &bars[kBbS + (j & 1)]);
         };
         if (ok && (ok = ring0(0))) scores(0);
         for (int j = 0; ok && j < n_iter; ++j) {
-          if (j > 0 && !(ok = dkey(j - 1))) break;
-          // dP over dS of the tile before, once it is consumed
-          ok = ring1(j) && (j == 0 || wait(&bars[kBbAcc0], (j - 1) & 1));
-          if (!ok) break;
-          mma_scores<HD>(tmem + L::kDP, a1, slot1(j));
-          mma_commit(&bars[kBbDP]);
-          ok = wait(&bars[kBbP], j & 1);
+          // dP over P and dS of the tile before, once they are consumed
+          ok = ring1(j) && (j == 0 || wait(&bars[kBbAcc + ((j - 1) & 1)], ((j - 1) >> 1) & 1));
           if (!ok) break;
           tc_fence_after();
-          mma_accumulate<HD>(tmem + L::kAcc1, tmem + L::kS0, slot1(j), j > 0);
-          mma_commit(&e1[j % kRing1]);
-          mma_commit(&bars[kBbAcc1]);
-          if (j + 1 < n_iter) {                     // S over P of this tile, once it is consumed
-            ok = ring0(j + 1) && wait(&bars[kBbAcc1], j & 1);
+          mma_scores<HD>(lead, tmem + (j & 1 ? L::kX0 : L::kX1), a1, slot1(j));
+          commit_if(lead, &bars[kBbDP + (j & 1)]);
+          if (j + 1 < n_iter) {                     // S over this dP, once it is read
+            ok = ring0(j + 1) && wait(&bars[kBbRd], j & 1);
             if (!ok) break;
+            tc_fence_after();
             scores(j + 1);
           }
         }
-        if (ok) dkey(n_iter - 1);
+      } else if (is_dq) {
+        for (int j = 0; ok && j < n_iter; ++j) {
+          ok = ring0(j) && wait(&bars[kBbDS + (j & 1)], (j >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_accumulate<HD>(lead, tmem + L::kAcc0, tmem + (j & 1 ? L::kS1 : L::kS0), 32, slot0(j), j > 0);
+          commit_if(lead, &bars[kBbAcc + (j & 1)]);
+          commit_if(lead, &e0[j % kRing0]);
+        }
+      } else {
+        for (int j = 0; ok && j < n_iter; ++j) {
+          const uint32_t x = tmem + (j & 1 ? L::kX1 : L::kX0);
+          ok = ring1(j) && wait(&bars[kBbP + (j & 1)], (j >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_accumulate<HD>(lead, tmem + L::kAcc1, x, 64, slot1(j), j > 0);
+          commit_if(lead, &e1[j % kRing1]);
+          ok = ring0(j) && wait(&bars[kBbDS + (j & 1)], (j >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_accumulate<HD>(lead, tmem + L::kAcc0, x + 32, 64, slot0(j), j > 0);
+          commit_if(lead, &bars[kBbAcc + (j & 1)]);
+          commit_if(lead, &e0[j % kRing0]);
+        }
       }
-      mma_commit(&bars[kBbDone]);
+      commit_if(lead, &bars[kBbDone]);
     }
   } else {
+    regs_inc<kBwdHighRegs>();
     // ------------------------------------------------------------ P and dS
-    const int wg = (warp - 3) >> 2;                 // columns [64 wg, 64 wg + 64)
+    const int wg = (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;           // row = tensor-memory lane
     const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = D.scale * 1.4426950408889634f;
     const float2 c2 = make_float2(c, c);
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, s_abort, limit));
-    };
     bool ok = run;
     if (is_dq) {
       const uint32_t bit = (BLK == 64 && r >= 64) ? 2u : 1u;
@@ -623,73 +715,87 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
         nd = b[64];
       }
       const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
-      // this tile's plan entry is read one tile ahead
-      auto entry = [&](int j) {
-        const int e = BLK == 64 ? 2 * (j - d0) + wg : j - d0;
-        return j >= d0 && j < n_iter && e < cnt ? entries[e] : 0u;
-      };
-      uint32_t pe = entry(0);
-      for (int j = 0; ok && j < n_iter; ++j) {
-        int v;                                      // valid key columns of this half
-        if (j < d0) {
-          v = max(0, min(64, D.ncur - j * 128 - wg * 64));
-        } else {
-          const int len = (pe & bit) ? block_len(D, (pe >> 4) & 0xFFF) : 0;
-          v = BLK == 64 ? len : max(0, min(64, len - wg * 64));
-        }
-        pe = entry(j + 1);
-        const uint32_t s_col = (j & 1 ? L::kS1 : L::kS0) + wg * 64;
-        if (!(ok = wait(&bars[kBbS + (j & 1)], (j >> 1) & 1))) break;
-        tc_fence_after();
-        float s[64];
-        if (v > 0) {
-          tmem_ld32(t_row + s_col, s);
-          tmem_ld32(t_row + s_col + 32, s + 32);
-          tmem_ld_wait();
-          reg_fence32(s);
-          reg_fence32(s + 32);
+      // valid key columns of each half of tile j for this row (the same for a warp's rows),
+      // v0 | v1 << 8; read one tile ahead
+      auto columns = [&](int j) {
+        if (j >= n_iter) return 0;
+        int v[2];
 #pragma unroll
-          for (int i = 0; i < 64; i += 2) {
+        for (int u = 0; u < 2; ++u) {
+          if (j < d0) {
+            v[u] = max(0, min(64, D.ncur - j * 128 - u * 64));
+          } else {
+            const int e = BLK == 64 ? 2 * (j - d0) + u : j - d0;
+            const uint32_t pe = e < cnt ? entries[e] : 0u;
+            const int len = (pe & bit) ? block_len(D, (pe >> 4) & 0xFFF) : 0;
+            v[u] = BLK == 64 ? len : max(0, min(64, len - u * 64));
+          }
+        }
+        return v[0] | v[1] << 8;
+      };
+      const uint32_t s_row = t_row + (wg ? L::kS1 : L::kS0);
+      int v_next = columns(wg);
+      for (int j = wg; ok && j < n_iter; j += 2) {
+        const int v[2] = {v_next & 255, v_next >> 8};
+        v_next = columns(j + 2);
+        if (!(ok = wait(&bars[kBbS + wg], (j >> 1) & 1))) break;
+        tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (v[u] > 0) {
+            tmem_ld32(s_row + u * 64, s + u * 64);
+            tmem_ld32(s_row + u * 64 + 32, s + u * 64 + 32);
+          }
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (v[u] == 0) continue;
+          reg_fence32(s + u * 64);
+          reg_fence32(s + u * 64 + 32);
+#pragma unroll
+          for (int i = u * 64; i < u * 64 + 64; i += 2) {
             const float2 x = ffma2(make_float2(s[i], s[i + 1]), c2, nl2);
             s[i] = ex2_approx(x.x);
             s[i + 1] = ex2_approx(x.y);
           }
         }
-        if (!(ok = wait(&bars[kBbDP], j & 1))) break;
+        if (!(ok = wait(&bars[kBbDP + wg], (j >> 1) & 1))) break;
         tc_fence_after();
-        if (v > 0) {
-          float g[64];
-          tmem_ld32(t_row + L::kDP + wg * 64, g);
-          tmem_ld32(t_row + L::kDP + wg * 64 + 32, g + 32);
-          tmem_ld_wait();
-          reg_fence32(g);
-          reg_fence32(g + 32);
-          warp_arrive(&bars[kBbP]);
 #pragma unroll
-          for (int i = 0; i < 64; i += 2) {
-            const float2 x = fadd2(make_float2(g[i], g[i + 1]), nd2);
-            s[i] *= x.x;
-            s[i + 1] *= x.y;
-          }
-          if (v < 64) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (i >= v) s[i] = 0.f;
-          }
-        } else {
-          warp_arrive(&bars[kBbP]);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) s[i] = 0.f;
-        }
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
+        for (int ch = 0; ch < 4; ++ch) {
+          const int u = ch >> 1;
           float pk[16];
+          if (v[u] > 0) {
+            float g[32];
+            tmem_ld32(t_row + L::kDP + ch * 32, g);
+            tmem_ld_wait();
+            reg_fence32(g);
+            if (ch == 3) warp_arrive(&bars[kBbRd]);
+            float* p = s + ch * 32;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(s[ch * 32 + 2 * e], s[ch * 32 + 2 * e + 1]);
-          tmem_st16(t_row + s_col + ch * 16, pk);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 x = fadd2(make_float2(g[i], g[i + 1]), nd2);
+              p[i] *= x.x;
+              p[i + 1] *= x.y;
+            }
+            if (v[u] < 64) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if ((ch & 1) * 32 + i >= v[u]) p[i] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
+          } else {
+            if (ch == 3) warp_arrive(&bars[kBbRd]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 0.f;
+          }
+          tmem_st16(s_row + ch * 16, pk);
         }
         tmem_st_wait();
-        warp_arrive(&bars[kBbDS + (j & 1)]);
+        warp_arrive(&bars[kBbDS + wg]);
       }
       const bool done = wait(&bars[kBbDone], 0);
       tc_fence_after();
@@ -706,17 +812,20 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
       for (int j = 0; ok && j < n_iter; ++j) {
         const bool on = (pe & bit) != 0;
         pe = entry(j + 1);
+        const uint32_t s_col = t_row + (j & 1 ? L::kX1 : L::kX0) + wg * 64;
+        const uint32_t p_col = t_row + (j & 1 ? L::kX0 : L::kX1) + wg * 64;
         const float4* nl4 = reinterpret_cast<const float4*>(
             smem + L::kCols + ((j & 1) * 2 + wg) * kBoxFloats * 4);
-        if (!(ok = wait(&bars[kBbS], j & 1))) break;
+        // the row values came with the ring slot that S is computed from; the issuer of S
+        // has waited for it, their readers have to as well (asynchronous copies)
+        ok = wait(&bars[kBbRing0 + j % kRing0], (j / kRing0) & 1) &&
+             wait(&bars[kBbS + (j & 1)], (j >> 1) & 1);
+        if (!ok) break;
         tc_fence_after();
         float s[64];
-        // the row values came with the ring slot that S was computed from; the issuer of S
-        // has waited for it, this thread has to as well (asynchronous copies)
-        if (!(ok = wait(&bars[kBbRing0 + j % kRing0], (j / kRing0) & 1))) break;
         if (on) {
-          tmem_ld32(t_row + L::kS0 + wg * 64, s);
-          tmem_ld32(t_row + L::kS0 + wg * 64 + 32, s + 32);
+          tmem_ld32(s_col, s);
+          tmem_ld32(s_col + 32, s + 32);
           tmem_ld_wait();
           reg_fence32(s);
           reg_fence32(s + 32);
@@ -730,43 +839,45 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
             s[i + 2] = ex2_approx(y.x);
             s[i + 3] = ex2_approx(y.y);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) s[i] = 0.f;
         }
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
           float pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(s[ch * 32 + 2 * e], s[ch * 32 + 2 * e + 1]);
-          tmem_st16(t_row + L::kS0 + wg * 64 + ch * 16, pk);
+          for (int e = 0; e < 16; ++e)
+            pk[e] = on ? pack_bf16(s[ch * 32 + 2 * e], s[ch * 32 + 2 * e + 1]) : 0.f;
+          tmem_st16(s_col + ch * 16, pk);
         }
         tmem_st_wait();
-        warp_arrive(&bars[kBbP]);
-        if (!(ok = wait(&bars[kBbDP], j & 1))) break;
+        warp_arrive(&bars[kBbP + (j & 1)]);
+        if (!(ok = wait(&bars[kBbDP + (j & 1)], (j >> 1) & 1))) break;
         tc_fence_after();
+        float g[64];
+        if (on) {
+          tmem_ld32(p_col, g);
+          tmem_ld32(p_col + 32, g + 32);
+          tmem_ld_wait();
+          reg_fence32(g);
+          reg_fence32(g + 32);
+        }
+        warp_arrive(&bars[kBbRd]);
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
           float pk[16];
           if (on) {
-            float g[32];
-            tmem_ld32(t_row + L::kDP + wg * 64 + ch * 32, g);
-            tmem_ld_wait();
-            reg_fence32(g);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 n = nl4[16 + ch * 8 + i / 4];
+            for (int i = ch * 32; i < ch * 32 + 32; i += 4) {
+              const float4 n = nl4[16 + i / 4];
               const float2 x = fadd2(make_float2(g[i], g[i + 1]), make_float2(n.x, n.y));
               const float2 y = fadd2(make_float2(g[i + 2], g[i + 3]), make_float2(n.z, n.w));
-              const float* p = s + ch * 32 + i;
-              pk[i / 2] = pack_bf16(p[0] * x.x, p[1] * x.y);
-              pk[i / 2 + 1] = pack_bf16(p[2] * y.x, p[3] * y.y);
+              pk[(i & 31) / 2] = pack_bf16(s[i] * x.x, s[i + 1] * x.y);
+              pk[(i & 31) / 2 + 1] = pack_bf16(s[i + 2] * y.x, s[i + 3] * y.y);
             }
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[e] = 0.f;
           }
-          tmem_st16(t_row + L::kDP + wg * 64 + ch * 16, pk);
+          tmem_st16(s_col + 32 + ch * 16, pk);
         }
         tmem_st_wait();
         warp_arrive(&bars[kBbDS + (j & 1)]);
@@ -791,7 +902,7 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
     if (lane == 0) mbar_wait_drain(&bars[kBbDone], 0, limit);
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(*s_tmem, 512);
   }
 }
 
