@@ -574,7 +574,7 @@ int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
   p.inv_off = w.inv_off;
   p.inv_cnt = w.inv_cnt;
   p.n_dq = lf::tile_count(D) * D.H;
-  p.wait_limit_ns = g_dbg_wait_limit_ns;
+  p.wait_limit_clk = 2 * (long long)g_dbg_wait_limit_ns;   // at up to 2 clocks per ns
   p.debug_stall = g_dbg_stall;
   for (int i = 0; i < D.S; ++i) p.slots[i] = sink_slots[i];
   for (int i = 0; i < D.F; ++i) p.slots[D.S + i] = hist_slots[i];

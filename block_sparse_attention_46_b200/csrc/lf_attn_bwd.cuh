@@ -266,7 +266,7 @@ struct BwdParams {
   const uint32_t* inv;
   const int32_t *inv_off, *inv_cnt;
   int n_dq;                   // query tiles of all heads
-  uint64_t wait_limit_ns;
+  long long wait_limit_clk;   // limit of a CTA's waits, from its start
   int debug_stall;            // test hook, as in the forward kernel
   int slots[LF_MAX_FRAMES];
 };
@@ -314,12 +314,25 @@ __device__ __forceinline__ uint32_t elect_lane() {
   return r;
 }
 
+// One product's MMAs (16 columns of A each), d (+)= A B with the first one's accumulation
+// given: A and B in shared memory, descriptors `step` apart, four to a 64-channel region.
+template <int N>
 __device__ __forceinline__ void mma_ss_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
-                                          uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead) : "memory");
+                                          uint32_t idesc, uint32_t region) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint64_t off = ((i >> 2) * region + (i & 3) * 32) >> 4;
+    if (i == 0)
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, 0, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+          "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+          ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(lead) : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.eq.b32 p, 0, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+          "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+          ::"r"(d), "l"(a + off), "l"(b + off), "r"(idesc), "r"(lead) : "memory");
+  }
 }
 
 __device__ __forceinline__ void mma_ts_if(uint32_t lead, uint32_t d, uint32_t a, uint64_t b,
@@ -386,12 +399,8 @@ __device__ __forceinline__ void load_box_if(uint32_t lead, uint8_t* tile, int bo
 template <int HD>
 __device__ __forceinline__ void mma_scores(uint32_t lead, uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
-  const uint64_t da = smem_desc_sw128(a, 16, 1024), db = smem_desc_sw128(b, 16, 1024);
-#pragma unroll
-  for (int ks = 0; ks < HD / 16; ++ks) {
-    const uint64_t off = ((ks >> 2) * BwdLayout<HD>::kRegion + (ks & 3) * 32) >> 4;
-    mma_ss_if(lead, d, da + off, db + off, idesc, ks > 0 ? 1u : 0u);
-  }
+  mma_ss_if<HD / 16>(lead, d, smem_desc_sw128(a, 16, 1024), smem_desc_sw128(b, 16, 1024), idesc,
+                     BwdLayout<HD>::kRegion);
 }
 
 // D (+)= A B over 128 columns of A: bf16 pairs in tensor memory, `half` columns between the
@@ -449,19 +458,30 @@ __device__ __forceinline__ void store_row(uint32_t taddr, float f, bool any, boo
   }
 }
 
-template <int HD, int BLK>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
+// Whole-warp wait for an mbarrier's phase, until the deadline (in clocks) at the latest.
+// Small, because the loops of all roles together have to stay within the 32 KB of the
+// instruction cache.
+__device__ __forceinline__ bool wait_until(uint64_t* bar, uint32_t parity, long long deadline) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 t;\n\t"
+      "W%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D%=;\n\t"
+      "mov.u64 t, %%clock64;\n\tsetp.lt.s64 q, t, %3;\n\t@q bra W%=;\n\t"
+      "D%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "l"(deadline) : "memory");
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+template <int HD, int BLK, bool is_dq>
+__device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, const int tile) {
   using L = BwdLayout<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kMisc);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint64_t limit = P.wait_limit_ns;
+  const long long deadline = clock64() + P.wait_limit_clk;
 
   // ---- the CTA's tile and the number of tiles that it streams
-  const bool is_dq = (int)blockIdx.x < P.n_dq;
   const int ntiles = tile_count(D);
   const int n_dense = D.kc > 0 ? 0 : cdiv(D.ncur, 128);
   int h, n_iter, cnt, qbA = 0, qbB = -1;
@@ -469,16 +489,16 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
   KeyTile kt{};
   int d0;                                           // tiles before this one are dense
   if (is_dq) {
-    const int t = blockIdx.x % ntiles;
-    h = blockIdx.x / ntiles;
+    const int t = tile % ntiles;
+    h = tile / ntiles;
     qbA = BLK == 64 ? 2 * t : t;
     if (BLK == 64 && 2 * t + 1 < D.nqb) qbB = 2 * t + 1;
-    cnt = P.plan_cnt[blockIdx.x];
-    entries = P.plan + (size_t)blockIdx.x * plan_stride(D);
+    cnt = P.plan_cnt[tile];
+    entries = P.plan + (size_t)tile * plan_stride(D);
     d0 = n_dense;
     n_iter = d0 + (BLK == 64 ? cdiv(cnt, 2) : cnt);
   } else {
-    kt = key_tile_of(blockIdx.x - P.n_dq, P.kt, D);
+    kt = key_tile_of(tile, P.kt, D);
     h = kt.h;
     if (kt.list < 0) {
       cnt = 0;
@@ -497,7 +517,6 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
       const bool rows = i == kBbP || i == kBbP + 1 || i == kBbRd || i == kBbDS || i == kBbDS + 1;
       mbar_init(&bars[i], rows ? (is_dq ? 4 : 8) : i == kBbDone ? 2 : 1);
     }
-    *s_abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -513,10 +532,13 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
   // the window of dynamic shared memory starts on 1024 bytes (swizzled tiles need it)
   const bool run = n_iter > 0 && (smem_u32(smem) & 1023u) == 0;
   if (n_iter > 0 && !run && threadIdx.x == 0) record_status(LF_ERR_CUDA);
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, s_abort, limit)) != 0;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_until(bar, parity, deadline); };
+  // for what has been issued and has to end before the CTA may exit: a limit of its own
+  auto drain = [&](uint64_t* bar, uint32_t parity) {
+    if (!wait_until(bar, parity, clock64() + P.wait_limit_clk) && lane == 0) record_status(LF_ERR_TIMEOUT);
   };
 
+  bool ok = run;                      // false for a warp once one of its waits has run out
   if (warp < 4) {
     regs_dec<kBwdLowRegs>();
     const uint32_t lead = elect_lane();
@@ -552,11 +574,12 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
         }
       }
       int j = 0, slot = 0, rnd = 0;
+#pragma unroll 1
       for (; run && j < n_iter; ++j) {
-        if (rnd > 0 && !wait(&empty[slot], (rnd & 1) ^ 1)) break;
+        if (rnd > 0 && !(ok = wait(&empty[slot], (rnd & 1) ^ 1))) break;
         // the row values' buffer of tile j - 2 has been read
         const bool cols = !is_dq && side0;
-        if (cols && j >= 2 && !wait(&bars[kBbDS + (j & 1)], ((j >> 1) & 1) ^ 1)) break;
+        if (cols && j >= 2 && !(ok = wait(&bars[kBbDS + (j & 1)], ((j >> 1) & 1) ^ 1))) break;
         expect_if(lead, &full[slot], L::kTile + (cols ? 2 * kBoxFloats * 4 : 0));
         uint8_t* dst = ring + slot * L::kTile;
         float* col = reinterpret_cast<float*>(smem + L::kCols) + (j & 1) * 2 * kBoxFloats;
@@ -604,9 +627,9 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
         if (++slot == n_slot) { slot = 0; ++rnd; }
       }
       // every copy issued lands before the CTA may exit
-      if (run && side0 && !stall) mbar_wait_drain(&bars[kBbIn], 0, limit);
+      if (run && side0 && !stall) drain(&bars[kBbIn], 0);
       for (int x = max(0, j - n_slot); x < j; ++x)
-        mbar_wait_drain(&full[x % n_slot], (x / n_slot) & 1, limit);
+        drain(&full[x % n_slot], (x / n_slot) & 1);
     } else {
       // ---------------------------------------------------------- MMA issuers
       const uint32_t a0 = smem_u32(in0), a1 = smem_u32(in1);
@@ -619,55 +642,35 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
       auto ring1 = [&](int j) { return wait(&f1[j % kRing1], (j / kRing1) & 1); };
       auto slot0 = [&](int j) { return r0 + (j % kRing0) * L::kTile; };
       auto slot1 = [&](int j) { return r1 + (j % kRing1) * L::kTile; };
-      bool ok = run && wait(&bars[kBbIn], 0);
-      if (warp == 1 && is_dq) {
-        auto scores = [&](int j) {
-          mma_scores<HD>(lead, tmem + (j & 1 ? L::kS1 : L::kS0), a0, slot0(j));
-          commit_if(lead, &bars[kBbS + (j & 1)]);
-        };
-        auto dprob = [&](int j) {
-          mma_scores<HD>(lead, tmem + L::kDP, a1, slot1(j));
-          commit_if(lead, &bars[kBbDP + (j & 1)]);
-          commit_if(lead, &e1[j % kRing1]);
-        };
-        if (ok && (ok = ring0(0))) scores(0);
-        if (ok && n_iter > 1 && (ok = ring0(1))) scores(1);
-        if (ok && (ok = ring1(0))) dprob(0);
-        for (int j = 0; ok && j < n_iter; ++j) {
-          if (j + 1 < n_iter) {                     // dP of the next tile, once this one's is read
-            ok = ring1(j + 1) && wait(&bars[kBbRd], j & 1);
+      ok = run && wait(&bars[kBbIn], 0);
+      if (warp == 1) {
+        // dq: S of tile j - 1 ahead; dP over dP of tile j - 1, once that is read; S over dS of
+        // tile j - 1, once that is consumed.  dk, dv: dP over P and dS of tile j - 1, once they
+        // are consumed; S over dP of tile j, once that is read.
+#pragma unroll 1
+        for (int j = is_dq ? -2 : -1; ok && j < n_iter; ++j) {
+          const int jp = is_dq ? j + 1 : j, js = is_dq ? j + 2 : j + 1;
+          if (jp >= 0 && jp < n_iter) {
+            ok = ring1(jp) && (is_dq ? j < 0 || wait(&bars[kBbRd], j & 1)
+                                     : j == 0 || wait(&bars[kBbAcc + ((j - 1) & 1)], ((j - 1) >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
-            dprob(j + 1);
+            mma_scores<HD>(lead, tmem + (is_dq ? L::kDP : j & 1 ? L::kX0 : L::kX1), a1, slot1(jp));
+            commit_if(lead, &bars[kBbDP + (jp & 1)]);
+            if (is_dq) commit_if(lead, &e1[jp % kRing1]);
           }
-          if (j + 2 < n_iter) {                     // S over dS of this tile, once it is consumed
-            ok = ring0(j + 2) && wait(&bars[kBbAcc + (j & 1)], (j >> 1) & 1);
+          if (js < n_iter) {
+            ok = ring0(js) && (is_dq ? j < 0 || wait(&bars[kBbAcc + (j & 1)], (j >> 1) & 1)
+                                     : j < 0 || wait(&bars[kBbRd], j & 1));
             if (!ok) break;
             tc_fence_after();
-            scores(j + 2);
-          }
-        }
-      } else if (warp == 1) {
-        auto scores = [&](int j) {
-          mma_scores<HD>(lead, tmem + (j & 1 ? L::kX1 : L::kX0), a0, slot0(j));
-          commit_if(lead, &bars[kBbS + (j & 1)]);
-        };
-        if (ok && (ok = ring0(0))) scores(0);
-        for (int j = 0; ok && j < n_iter; ++j) {
-          // dP over P and dS of the tile before, once they are consumed
-          ok = ring1(j) && (j == 0 || wait(&bars[kBbAcc + ((j - 1) & 1)], ((j - 1) >> 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          mma_scores<HD>(lead, tmem + (j & 1 ? L::kX0 : L::kX1), a1, slot1(j));
-          commit_if(lead, &bars[kBbDP + (j & 1)]);
-          if (j + 1 < n_iter) {                     // S over this dP, once it is read
-            ok = ring0(j + 1) && wait(&bars[kBbRd], j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            scores(j + 1);
+            mma_scores<HD>(lead, tmem + (is_dq ? (js & 1 ? L::kS1 : L::kS0) : js & 1 ? L::kX1 : L::kX0), a0,
+                           slot0(js));
+            commit_if(lead, &bars[kBbS + (js & 1)]);
           }
         }
       } else if (is_dq) {
+#pragma unroll 1
         for (int j = 0; ok && j < n_iter; ++j) {
           ok = ring0(j) && wait(&bars[kBbDS + (j & 1)], (j >> 1) & 1);
           if (!ok) break;
@@ -677,19 +680,21 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
           commit_if(lead, &e0[j % kRing0]);
         }
       } else {
+#pragma unroll 1
         for (int j = 0; ok && j < n_iter; ++j) {
           const uint32_t x = tmem + (j & 1 ? L::kX1 : L::kX0);
           ok = ring1(j) && wait(&bars[kBbP + (j & 1)], (j >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           mma_accumulate<HD>(lead, tmem + L::kAcc1, x, 64, slot1(j), j > 0);
-          commit_if(lead, &e1[j % kRing1]);
           ok = ring0(j) && wait(&bars[kBbDS + (j & 1)], (j >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           mma_accumulate<HD>(lead, tmem + L::kAcc0, x + 32, 64, slot0(j), j > 0);
           commit_if(lead, &bars[kBbAcc + (j & 1)]);
           commit_if(lead, &e0[j % kRing0]);
+          // dout's slot only now: dP, the other issuer's, may end after dv, but dS follows it
+          commit_if(lead, &e1[j % kRing1]);
         }
       }
       commit_if(lead, &bars[kBbDone]);
@@ -701,8 +706,6 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
     const int r = (warp & 3) * 32 + lane;           // row = tensor-memory lane
     const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = D.scale * 1.4426950408889634f;
-    const float2 c2 = make_float2(c, c);
-    bool ok = run;
     if (is_dq) {
       const uint32_t bit = (BLK == 64 && r >= 64) ? 2u : 1u;
       const int qb = BLK == 64 ? (r < 64 ? qbA : qbB) : qbA, i0 = BLK == 64 ? (r & 63) : r;
@@ -714,7 +717,6 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
         nl = b[0];
         nd = b[64];
       }
-      const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
       // valid key columns of each half of tile j for this row (the same for a warp's rows),
       // v0 | v1 << 8; read one tile ahead
       auto columns = [&](int j) {
@@ -735,71 +737,57 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
       };
       const uint32_t s_row = t_row + (wg ? L::kS1 : L::kS0);
       int v_next = columns(wg);
+#pragma unroll 1
       for (int j = wg; ok && j < n_iter; j += 2) {
-        const int v[2] = {v_next & 255, v_next >> 8};
+        const int v = v_next;
         v_next = columns(j + 2);
         if (!(ok = wait(&bars[kBbS + wg], (j >> 1) & 1))) break;
         tc_fence_after();
-        float s[128];
+        // P in fp32 over S, then dS, in loops of 32 columns: code that stays in the
+        // instruction cache is worth more here than values that stay in registers
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          const int nv = (v >> (ch >> 1) * 8 & 255) - (ch & 1) * 32;   // valid columns from here on
+          if (nv <= 0) continue;
+          float s[32];
+          tmem_ld32(s_row + ch * 32, s);
+          tmem_ld_wait();
+          reg_fence32(s);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (v[u] > 0) {
-            tmem_ld32(s_row + u * 64, s + u * 64);
-            tmem_ld32(s_row + u * 64 + 32, s + u * 64 + 32);
+          for (int i = 0; i < 32; ++i) s[i] = ex2_approx(fmaf(s[i], c, nl));
+          if (nv < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= nv) s[i] = 0.f;
           }
-        }
-        tmem_ld_wait();
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (v[u] == 0) continue;
-          reg_fence32(s + u * 64);
-          reg_fence32(s + u * 64 + 32);
-#pragma unroll
-          for (int i = u * 64; i < u * 64 + 64; i += 2) {
-            const float2 x = ffma2(make_float2(s[i], s[i + 1]), c2, nl2);
-            s[i] = ex2_approx(x.x);
-            s[i + 1] = ex2_approx(x.y);
-          }
+          tmem_st32(s_row + ch * 32, s);
         }
         if (!(ok = wait(&bars[kBbDP + wg], (j >> 1) & 1))) break;
         tc_fence_after();
-#pragma unroll
+        tmem_st_wait();
+#pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
-          const int u = ch >> 1;
-          float pk[16];
-          if (v[u] > 0) {
-            float g[32];
+          float s[32], g[32], pk[16];
+          const bool any = (v >> (ch >> 1) * 8 & 255) > (ch & 1) * 32;
+          if (any) {
+            tmem_ld32(s_row + ch * 32, s);
             tmem_ld32(t_row + L::kDP + ch * 32, g);
             tmem_ld_wait();
+            reg_fence32(s);
             reg_fence32(g);
-            if (ch == 3) warp_arrive(&bars[kBbRd]);
-            float* p = s + ch * 32;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 x = fadd2(make_float2(g[i], g[i + 1]), nd2);
-              p[i] *= x.x;
-              p[i + 1] *= x.y;
-            }
-            if (v[u] < 64) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if ((ch & 1) * 32 + i >= v[u]) p[i] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
-          } else {
-            if (ch == 3) warp_arrive(&bars[kBbRd]);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = 0.f;
           }
+          if (ch == 3) warp_arrive(&bars[kBbRd]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            pk[i] = any ? pack_bf16(s[2 * i] * (g[2 * i] + nd), s[2 * i + 1] * (g[2 * i + 1] + nd)) : 0.f;
           tmem_st16(s_row + ch * 16, pk);
         }
         tmem_st_wait();
         warp_arrive(&bars[kBbDS + wg]);
       }
-      const bool done = wait(&bars[kBbDone], 0);
+      if (run) ok = wait(&bars[kBbDone], 0) && ok;
       tc_fence_after();
-      if ((ok || n_iter == 0) && done)
+      if (ok || n_iter == 0)
         store_row<HD / 2>(t_row + L::kAcc0 + wg * (HD / 2), D.scale, n_iter > 0, valid,
                           P.dq + ((size_t)tok * D.H + h) * HD + wg * (HD / 2));
     } else {
@@ -809,6 +797,7 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
         return j < d0 ? 3u : j < n_iter && e < cnt ? entries[e] : 0u;
       };
       uint32_t pe = entry(0);
+#pragma unroll 1
       for (int j = 0; ok && j < n_iter; ++j) {
         const bool on = (pe & bit) != 0;
         pe = entry(j + 1);
@@ -832,12 +821,10 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
             const float4 n = nl4[i / 4];
-            const float2 x = ffma2(make_float2(s[i], s[i + 1]), c2, make_float2(n.x, n.y));
-            const float2 y = ffma2(make_float2(s[i + 2], s[i + 3]), c2, make_float2(n.z, n.w));
-            s[i] = ex2_approx(x.x);
-            s[i + 1] = ex2_approx(x.y);
-            s[i + 2] = ex2_approx(y.x);
-            s[i + 3] = ex2_approx(y.y);
+            s[i] = ex2_approx(fmaf(s[i], c, n.x));
+            s[i + 1] = ex2_approx(fmaf(s[i + 1], c, n.y));
+            s[i + 2] = ex2_approx(fmaf(s[i + 2], c, n.z));
+            s[i + 3] = ex2_approx(fmaf(s[i + 3], c, n.w));
           }
         }
 #pragma unroll
@@ -868,10 +855,8 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
 #pragma unroll
             for (int i = ch * 32; i < ch * 32 + 32; i += 4) {
               const float4 n = nl4[16 + i / 4];
-              const float2 x = fadd2(make_float2(g[i], g[i + 1]), make_float2(n.x, n.y));
-              const float2 y = fadd2(make_float2(g[i + 2], g[i + 3]), make_float2(n.z, n.w));
-              pk[(i & 31) / 2] = pack_bf16(s[i] * x.x, s[i + 1] * x.y);
-              pk[(i & 31) / 2 + 1] = pack_bf16(s[i + 2] * y.x, s[i + 3] * y.y);
+              pk[(i & 31) / 2] = pack_bf16(s[i] * (g[i] + n.x), s[i + 1] * (g[i + 1] + n.y));
+              pk[(i & 31) / 2 + 1] = pack_bf16(s[i + 2] * (g[i + 2] + n.z), s[i + 3] * (g[i + 3] + n.w));
             }
           } else {
 #pragma unroll
@@ -882,9 +867,9 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
         tmem_st_wait();
         warp_arrive(&bars[kBbDS + (j & 1)]);
       }
-      const bool done = wait(&bars[kBbDone], 0);
+      if (run) ok = wait(&bars[kBbDone], 0) && ok;
       tc_fence_after();
-      if ((ok || n_iter == 0) && done) {
+      if (ok || n_iter == 0) {
         const bool cur = kt.kind == 0 || kt.kind == 2;
         const bool valid = kt.row + r < (kt.kind == 0 ? D.ncur : D.T);
         const size_t tok = (size_t)kt.row + r + (kt.kind == 0 ? 0
@@ -897,13 +882,20 @@ attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
     }
     tc_fence_before();
   }
+  if (run && !ok && lane == 0) record_status(LF_ERR_TIMEOUT);
   __syncthreads();
   if (warp == 1) {
-    if (lane == 0) mbar_wait_drain(&bars[kBbDone], 0, limit);
-    __syncwarp();
+    drain(&bars[kBbDone], 0);
     tc_fence_after();
     tmem_dealloc(*s_tmem, 512);
   }
+}
+
+template <int HD, int BLK>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+attn_bwd_kernel(const __grid_constant__ BwdParams P, const Dims D) {
+  if ((int)blockIdx.x < P.n_dq) bwd_tile<HD, BLK, true>(P, D, blockIdx.x);
+  else bwd_tile<HD, BLK, false>(P, D, blockIdx.x - P.n_dq);
 }
 
 }  // namespace lf
