@@ -258,7 +258,7 @@ struct BwdParams {
   // rows of H * d channels: 2-D over the chunk's tokens, boxes of 64 channels x 128 rows, and
   // 3-D per frame, boxes of 64 x 64
   CUtensorMap q2, q3, g2, g3, kc2, kc3, vc2, vc3, kh, vh;
-  __nv_bfloat16 *dq, *dk_cur, *dv_cur, *dk_cache, *dv_cache;
+  CUtensorMap dq3, dk2, dk3, dkh, dv2, dv3, dvh;   // outputs, boxes of 64 x 64
   const uint32_t* plan;
   const int32_t* plan_cnt;
   BwdRows rows;
@@ -285,6 +285,7 @@ enum BwdBar {
   kBbCount = 23
 };
 constexpr int kRing0 = 3, kRing1 = 2;
+constexpr int kNbStore = 1;            // named barriers of a warpgroup's epilogue, + warpgroup
 
 template <int HD>
 struct BwdLayout {
@@ -429,11 +430,11 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// N accumulators of a row, times f, as bf16 (zeros when !any).
+// N (64 or 128) accumulators of a row, times f, as bf16 (zeros when !any) into the row of a
+// tile in shared memory, in the 128-byte swizzle of the tensor maps.
 template <int N>
-__device__ __forceinline__ void store_row(uint32_t taddr, float f, bool any, bool store,
-                                          __nv_bfloat16* dst) {
-#pragma unroll
+__device__ __forceinline__ void stage_row(uint8_t* tile, int r, uint32_t taddr, float f, bool any) {
+#pragma unroll 1
   for (int ch = 0; ch < N / 32; ++ch) {
     float v[32];
     if (any) {
@@ -444,18 +445,33 @@ __device__ __forceinline__ void store_row(uint32_t taddr, float f, bool any, boo
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0.f;
     }
-    if (store) {
+    uint8_t* row = tile + (ch >> 1) * (128 * 128) + r * 128;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint4 w;
-        w.x = __float_as_uint(pack_bf16(v[8 * e] * f, v[8 * e + 1] * f));
-        w.y = __float_as_uint(pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f));
-        w.z = __float_as_uint(pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f));
-        w.w = __float_as_uint(pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f));
-        reinterpret_cast<uint4*>(dst)[ch * 4 + e] = w;
-      }
+    for (int e = 0; e < 4; ++e) {
+      uint4 w;
+      w.x = __float_as_uint(pack_bf16(v[8 * e] * f, v[8 * e + 1] * f));
+      w.y = __float_as_uint(pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f));
+      w.z = __float_as_uint(pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f));
+      w.w = __float_as_uint(pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f));
+      *reinterpret_cast<uint4*>(row + ((((ch & 1) * 4 + e) ^ (r & 7)) << 4)) = w;
     }
   }
+}
+
+// 64 rows x 64 channels of a staged tile to memory; what lies past the tensor's (or frame's)
+// end is not written.
+__device__ __forceinline__ void store_box(const void* src, const CUtensorMap* m, int x, int row, int frame) {
+  if (frame < 0)
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(m), "r"(smem_u32(src)), "r"(x), "r"(row) : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(m), "r"(smem_u32(src)), "r"(x), "r"(row), "r"(frame) : "memory");
+}
+
+// The stores issued by this thread have read shared memory, and their writes are done.
+__device__ __forceinline__ void stores_done() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Whole-warp wait for an mbarrier's phase, until the deadline (in clocks) at the latest.
@@ -787,9 +803,19 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
       }
       if (run) ok = wait(&bars[kBbDone], 0) && ok;
       tc_fence_after();
-      if (ok || n_iter == 0)
-        store_row<HD / 2>(t_row + L::kAcc0 + wg * (HD / 2), D.scale, n_iter > 0, valid,
-                          P.dq + ((size_t)tok * D.H + h) * HD + wg * (HD / 2));
+      // 64 channels each (d = 64: the first warpgroup alone), over Q, which no MMA reads any more
+      const bool mine = HD == 128 || wg == 0;
+      if (mine && (ok || n_iter == 0)) {
+        stage_row<64>(in0 + wg * L::kRegion, r, t_row + L::kAcc0 + wg * 64, D.scale, n_iter > 0);
+        fence_proxy_async_smem();
+      }
+      named_bar_sync(kNbStore + wg, 128);
+      if (mine && (ok || n_iter == 0) && r < 2) {   // a box each
+        const int q2 = BLK == 64 && r ? qbB : qbA, row = (q2 % D.nbpf) * BLK + (BLK == 128 ? r * 64 : 0);
+        if (q2 >= 0 && row < D.T)
+          store_box(in0 + wg * L::kRegion + r * 64 * 128, &P.dq3, h * HD + wg * 64, row, q2 / D.nbpf);
+        stores_done();
+      }
     } else {
       const uint32_t bit = r < 64 ? 1u : 2u;
       auto entry = [&](int j) {                     // dense: every row attends
@@ -869,15 +895,23 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
       }
       if (run) ok = wait(&bars[kBbDone], 0) && ok;
       tc_fence_after();
+      // dk over K and dv over V, which no MMA reads any more
+      uint8_t* out = wg == 0 ? in0 : in1;
       if (ok || n_iter == 0) {
-        const bool cur = kt.kind == 0 || kt.kind == 2;
-        const bool valid = kt.row + r < (kt.kind == 0 ? D.ncur : D.T);
-        const size_t tok = (size_t)kt.row + r + (kt.kind == 0 ? 0
-                           : (size_t)(kt.kind == 2 ? kt.frame
-                                      : P.slots[kt.kind == 1 ? kt.frame : D.S + kt.frame]) * D.T);
-        __nv_bfloat16* dst = wg == 0 ? (cur ? P.dk_cur : P.dk_cache) : (cur ? P.dv_cur : P.dv_cache);
-        store_row<HD>(t_row + (wg == 0 ? L::kAcc0 : L::kAcc1), wg == 0 ? D.scale : 1.f, n_iter > 0,
-                      valid, dst + (tok * D.H + h) * HD);
+        stage_row<HD>(out, r, t_row + (wg == 0 ? L::kAcc0 : L::kAcc1), wg == 0 ? D.scale : 1.f, n_iter > 0);
+        fence_proxy_async_smem();
+      }
+      named_bar_sync(kNbStore + wg, 128);
+      if ((ok || n_iter == 0) && r < 2) {           // a box each
+        const int row = kt.row + r * 64;
+        const int f = kt.kind == 0 ? -1 : kt.kind == 2 ? kt.frame
+                                        : P.slots[kt.kind == 1 ? kt.frame : D.S + kt.frame];
+        const CUtensorMap* m = wg == 0 ? (kt.kind == 0 ? &P.dk2 : kt.kind == 2 ? &P.dk3 : &P.dkh)
+                                       : (kt.kind == 0 ? &P.dv2 : kt.kind == 2 ? &P.dv3 : &P.dvh);
+        if (row < (kt.kind == 0 ? D.ncur : D.T))
+          for (int c = 0; c < L::NH; ++c)
+            store_box(out + c * L::kRegion + r * 64 * 128, m, h * HD + c * 64, row, f);
+        stores_done();
       }
     }
     tc_fence_before();
