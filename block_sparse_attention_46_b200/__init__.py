@@ -8,6 +8,7 @@ does not load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -31,6 +32,7 @@ __all__ = [
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblf.so")
 
 LF_OK = 0
+LF_ERR_INVALID_ARG = 1
 
 
 class LfError(RuntimeError):
@@ -389,26 +391,49 @@ def lf_forward_chunk(shape, q, k_cur, v_cur, k_cache, v_cache, hist_slots, sink_
 
 
 # ------------------------------------------------------------------ gradient, rotary positions
-def _on(device, what, dtype, count, **tensors):
-    """Checks what the C side cannot see of the given tensors: one device, type and size."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device != device:
-            raise ValueError(f"{what}: {name} is on {t.device}, not {device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{what}: {name} is {t.dtype}, not {dtype}")
-        if count is not None and t.numel() != count:
-            raise ValueError(f"{what}: {name} has {t.numel()} elements, not {count}")
+# These calls are small next to what they launch only when their checks are: one look at each
+# tensor, plain integers for pointers, the device switched only when it is another one.
+def _arg(what, name, t, device, dtype, count=None):
+    """Address of a contiguous tensor after checking what the C side cannot see of it: its
+    device, type and number of elements.  None stays None."""
+    if t is None:
+        return None
+    if t.device != device or t.dtype != dtype:
+        raise ValueError(f"{what}: {name} is {t.dtype} on {t.device}, not {dtype} on {device}")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{what}: {name} has {t.numel()} elements, not {count}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be contiguous")
+    return t.data_ptr()
 
 
-def _workspace(workspace, size, device, stream):
-    """The caller's workspace, or one of `size` bytes from the memory of the stream that the
-    call runs on, which may be reused once that stream is past the call."""
-    if workspace is None and size > 0:
+def _on_gpu(what, name, t):
+    if t is None or t.device.type != "cuda":
+        raise ValueError(f"{what}: {name} must be a CUDA tensor")
+    return t.device
+
+
+def _device(device):
+    """Makes `device` current for a call, if it is not."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _stream_handle(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _workspace(what, workspace, size, device, stream):
+    """(tensor, address, bytes): the caller's workspace, or one of size() bytes from the memory
+    of the stream that the call runs on, which may be reused once that stream is past the call."""
+    if workspace is None:
+        n = size()
+        if n == 0:
+            return None, None, 0
         with torch.cuda.stream(stream):               # None: the current stream
-            workspace = torch.empty(size, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+            workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    return workspace, _arg(what, "workspace", workspace, device, torch.uint8), workspace.numel()
 
 
 def lf_attn_backward_workspace_size(shape) -> int:
@@ -423,34 +448,35 @@ def lf_block_sparse_attn_backward(shape, q, k_cur, v_cur, k_cache, v_cache, hist
     """Gradient of lf_block_sparse_attn (or of the attention of lf_forward_chunk): dq, dk_cur
     and dv_cur, and with dk_cache and dv_cache the gradient into the listed cache slots, from
     the forward call's out and lse and the gradient dout of out."""
-    sh = make_shape(shape)
     what = "lf_block_sparse_attn_backward"
-    dev, bf = q.device, torch.bfloat16
-    if len(hist_slots) != shape.n_hist or len(sink_slots) != shape.n_sink:
+    sh = make_shape(shape)
+    dev, bf, i32 = _on_gpu(what, "q", q), torch.bfloat16, torch.int32
+    if len(hist_slots) != sh.n_hist or len(sink_slots) != sh.n_sink:
         raise ValueError(f"{what}: slot lists do not match the shape's frames")
     _, nqb, kf, kb = derived(shape)
-    ncur = shape.n_cur_frames * shape.T
-    cached = shape.n_slots * shape.T * shape.H * shape.d
-    _on(dev, what, bf, ncur * shape.H * shape.d, q=q, k_cur=k_cur, v_cur=v_cur, out=out,
-        dout=dout, dq=dq, dk_cur=dk_cur, dv_cur=dv_cur)
-    _on(dev, what, torch.float32, shape.H * ncur, lse=lse)
-    if shape.n_hist + shape.n_sink > 0:
-        _on(dev, what, bf, cached, k_cache=k_cache, v_cache=v_cache, dk_cache=dk_cache,
-            dv_cache=dv_cache)
-    if shape.n_hist > 0:
-        _on(dev, what, torch.int32, shape.H * nqb * kf * kb, block_idx=block_idx)
-    if current_blocks(shape) > 0:
-        _on(dev, what, torch.int32, shape.H * nqb * current_blocks(shape), cur_idx=cur_idx)
+    row = sh.H * sh.d
+    chunk = sh.n_cur_frames * sh.tokens_per_frame * row
+    cached = sh.n_slots * sh.tokens_per_frame * row if sh.n_hist + sh.n_sink > 0 else None
+    cur = [_arg(what, n, t, dev, bf, chunk) for n, t in
+           (("q", q), ("k_cur", k_cur), ("v_cur", v_cur), ("out", out), ("dout", dout),
+            ("dq", dq), ("dk_cur", dk_cur), ("dv_cur", dv_cur))]
+    cache = [_arg(what, n, t, dev, bf, cached) for n, t in
+             (("k_cache", k_cache), ("v_cache", v_cache), ("dk_cache", dk_cache),
+              ("dv_cache", dv_cache))]
+    p_lse = _arg(what, "lse", lse, dev, torch.float32, chunk // sh.d)
+    p_bi = _arg(what, "block_idx", block_idx, dev, i32, sh.H * nqb * kf * kb) if sh.n_hist else None
+    kc = current_blocks(shape)
+    p_ci = _arg(what, "cur_idx", cur_idx, dev, i32, sh.H * nqb * kc) if kc else None
     hs, _k1 = _slots(hist_slots)
     ss, _k2 = _slots(sink_slots)
-    with torch.cuda.device(dev):
-        workspace, size = _workspace(workspace, lf_attn_backward_workspace_size(shape), dev, stream)
-        _on(dev, what, torch.uint8, None, workspace=workspace)
-        _check(load().lf_block_sparse_attn_backward(
-            ctypes.byref(sh), _ptr(q), _ptr(k_cur), _ptr(v_cur), _ptr(k_cache), _ptr(v_cache), hs,
-            ss, _ptr(block_idx), _ptr(cur_idx), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq),
-            _ptr(dk_cur), _ptr(dv_cur), _ptr(dk_cache), _ptr(dv_cache), _ptr(workspace), size,
-            _stream(stream)), what)
+    lib = load()
+    with _device(dev):
+        _ws, p_ws, n_ws = _workspace(
+            what, workspace, lambda: lib.lf_attn_backward_workspace_size(ctypes.byref(sh)), dev, stream)
+        _check(lib.lf_block_sparse_attn_backward(
+            ctypes.byref(sh), cur[0], cur[1], cur[2], cache[0], cache[1], hs, ss, p_bi, p_ci,
+            cur[3], cur[4], p_lse, cur[5], cur[6], cur[7], cache[2], cache[3], p_ws, n_ws,
+            _stream_handle(stream)), what)
 
 
 _NORMS = {None: 0, "head": 1, "token": 2, "row": 2}
@@ -466,60 +492,60 @@ def make_rope(H, d, n_frames, height, width, pairs, halves=False, norm=None, bas
                   _NORMS[norm], eps, base)
 
 
-def _rope_tokens(rope, t, name, contiguous):
-    """(pointer, elements between tokens, frames) of bf16 tokens [..., H, d] whose leading
+def _rope_tokens(H, d, T, t, name, device, contiguous):
+    """(address, elements between tokens, frames) of bf16 tokens [..., H, d] whose leading
     dimensions are frames x tokens at one stride."""
     what = "lf_rope"
-    if not t.is_cuda or t.dtype != torch.bfloat16:
-        raise ValueError(f"{what}: {name} must be a bf16 CUDA tensor")
-    T = rope.height * rope.width
-    if t.dim() < 3 or tuple(t.shape[-2:]) != (rope.H, rope.d) or t.numel() % (T * rope.H * rope.d):
-        raise ValueError(f"{what}: {name} must be [frames, {T}, {rope.H}, {rope.d}] or "
-                         f"[frames * {T}, {rope.H}, {rope.d}]")
-    n = t.numel() // (rope.H * rope.d)
-    stride = rope.H * rope.d
-    sizes = [(s, st) for s, st in zip(t.shape[:-2], t.stride()[:-2]) if s != 1]
-    if sizes:
-        stride = sizes[-1][1]
-    step = stride
-    for s, st in reversed(sizes):
+    if t.device != device or t.dtype != torch.bfloat16:
+        raise ValueError(f"{what}: {name} is {t.dtype} on {t.device}, not bf16 on {device}")
+    shape, row = t.shape, H * d
+    n, rest = divmod(t.numel(), T * row)
+    if len(shape) < 3 or shape[-2] != H or shape[-1] != d or rest:
+        raise ValueError(f"{what}: {name} must be [frames, {T}, {H}, {d}] or [frames * {T}, {H}, {d}]")
+    if t.is_contiguous():
+        return t.data_ptr(), row, n
+    if contiguous:
+        raise ValueError(f"{what}: {name} must be contiguous")
+    strides = t.stride()
+    if (strides[-1] != 1 and d > 1) or (strides[-2] != d and H > 1):
+        raise ValueError(f"{what}: a token's H * d channels of {name} must be contiguous")
+    stride = step = 0
+    for s, st in zip(shape[-3::-1], strides[-3::-1]):
+        if s == 1:
+            continue
+        if step == 0:
+            stride = step = st
         if st != step:
             raise ValueError(f"{what}: {name}'s tokens are not at one stride")
         step *= s
-    if (t.stride(-1) != 1 and rope.d > 1) or (t.stride(-2) != rope.d and rope.H > 1):
-        raise ValueError(f"{what}: a token's H * d channels of {name} must be contiguous")
-    if contiguous and stride != rope.H * rope.d:
-        raise ValueError(f"{what}: {name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), stride, n // T
+    return t.data_ptr(), stride or row, n
 
 
-def _frames(rope, v, name):
+def _frames(n_frames, v, name):
     if v is None:
         return None, None
-    if len(v) != rope.n_frames:
+    if len(v) != n_frames:
         raise ValueError(f"lf_rope: {name} needs one entry per frame")
     return _slots(v)
-
-
-def _rope_weight(rope, device, **tensors):
-    n = rope.d if rope.norm == 1 else rope.H * rope.d
-    _on(device, "lf_rope", torch.float32, n, **tensors)
 
 
 def lf_rope_frames(rope, x, out, frame_pos=None, weight=None, in_slots=None, out_slots=None,
                    stream=None):
     """Norm and rotary positions of n_frames frames of x [n_in, T, H, d] (tokens may lie
     inside a wider projection) into out [n_out, T, H, d], through optional slot lists."""
-    px, xs, n_in = _rope_tokens(rope, x, "x", False)
-    po, _, n_out = _rope_tokens(rope, out, "out", True)
-    _rope_weight(rope, x.device, weight=weight)
-    _on(x.device, "lf_rope", torch.bfloat16, None, out=out)
-    si, _k1 = _frames(rope, in_slots, "in_slots")
-    so, _k2 = _frames(rope, out_slots, "out_slots")
-    fp, _k3 = _frames(rope, frame_pos, "frame_pos")
-    with torch.cuda.device(x.device):
-        _check(load().lf_rope_frames(ctypes.byref(rope), px, xs, n_in, si, fp, _ptr(weight), po,
-                                     n_out, so, _stream(stream)), "lf_rope_frames")
+    dev = _on_gpu("lf_rope", "x", x)
+    H, d, T, F, norm = rope.H, rope.d, rope.height * rope.width, rope.n_frames, rope.norm
+    if H < 1 or d < 1 or T < 1:
+        _check(LF_ERR_INVALID_ARG, "lf_rope_frames")
+    px, xs, n_in = _rope_tokens(H, d, T, x, "x", dev, False)
+    po, _, n_out = _rope_tokens(H, d, T, out, "out", dev, True)
+    pw = _arg("lf_rope", "weight", weight, dev, torch.float32, d if norm == 1 else H * d)
+    si, _k1 = _frames(F, in_slots, "in_slots")
+    so, _k2 = _frames(F, out_slots, "out_slots")
+    fp, _k3 = _frames(F, frame_pos, "frame_pos")
+    with _device(dev):
+        _check(load().lf_rope_frames(ctypes.byref(rope), px, xs, n_in, si, fp, pw, po, n_out, so,
+                                     _stream_handle(stream)), "lf_rope_frames")
 
 
 def lf_rope_backward_workspace_size(rope) -> int:
@@ -530,22 +556,28 @@ def lf_rope_frames_backward(rope, x, dout, dx, frame_pos=None, weight=None, dwei
                             in_slots=None, out_slots=None, workspace=None, stream=None):
     """Gradient of lf_rope_frames: dx (x's frames and slots, its own token stride) and, with a
     norm, dweight, from dout.  x may be None without a norm."""
+    dev = _on_gpu("lf_rope", "dx", dx)
+    H, d, T, F, norm = rope.H, rope.d, rope.height * rope.width, rope.n_frames, rope.norm
+    if H < 1 or d < 1 or T < 1:
+        _check(LF_ERR_INVALID_ARG, "lf_rope_frames_backward")
     px, xs = None, 0
-    pd, ds, n_in = _rope_tokens(rope, dx, "dx", False)
+    pd, ds, n_in = _rope_tokens(H, d, T, dx, "dx", dev, False)
     if x is not None:
-        px, xs, n_x = _rope_tokens(rope, x, "x", False)
+        px, xs, n_x = _rope_tokens(H, d, T, x, "x", dev, False)
         if n_x != n_in:
             raise ValueError("lf_rope: x and dx differ in frames")
-    pg, _, n_out = _rope_tokens(rope, dout, "dout", True)
-    _rope_weight(rope, dx.device, weight=weight, dweight=dweight)
-    _on(dx.device, "lf_rope", torch.bfloat16, None, x=x, dout=dout)
-    si, _k1 = _frames(rope, in_slots, "in_slots")
-    so, _k2 = _frames(rope, out_slots, "out_slots")
-    fp, _k3 = _frames(rope, frame_pos, "frame_pos")
-    with torch.cuda.device(dx.device):
-        workspace, size = _workspace(workspace, lf_rope_backward_workspace_size(rope), dx.device,
-                                     stream)
-        _on(dx.device, "lf_rope", torch.uint8, None, workspace=workspace)
-        _check(load().lf_rope_frames_backward(
-            ctypes.byref(rope), px, xs, n_in, si, fp, _ptr(weight), pg, n_out, so, pd, ds,
-            _ptr(dweight), _ptr(workspace), size, _stream(stream)), "lf_rope_frames_backward")
+    pg, _, n_out = _rope_tokens(H, d, T, dout, "dout", dev, True)
+    n_w = d if norm == 1 else H * d
+    pw = _arg("lf_rope", "weight", weight, dev, torch.float32, n_w)
+    pdw = _arg("lf_rope", "dweight", dweight, dev, torch.float32, n_w)
+    si, _k1 = _frames(F, in_slots, "in_slots")
+    so, _k2 = _frames(F, out_slots, "out_slots")
+    fp, _k3 = _frames(F, frame_pos, "frame_pos")
+    lib = load()
+    with _device(dev):
+        _ws, p_ws, size = _workspace(
+            "lf_rope", workspace, lambda: lib.lf_rope_backward_workspace_size(ctypes.byref(rope)),
+            dev, stream)
+        _check(lib.lf_rope_frames_backward(
+            ctypes.byref(rope), px, xs, n_in, si, fp, pw, pg, n_out, so, pd, ds, pdw, p_ws, size,
+            _stream_handle(stream)), "lf_rope_frames_backward")

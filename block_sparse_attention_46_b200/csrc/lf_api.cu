@@ -591,10 +591,12 @@ int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
 }
 
 // ---------------------------------------------------------------- rotary positions
+using RopeCall = lf::RopeArgs<LF_MAX_FRAMES>;
+
 // Validates a rotary call's sizes and lists and fills the kernel's arguments but for the
 // tensors.  Lists are host arrays of n_frames, or null for 0, 1, ...
 int make_rope(const lf_rope* r, int32_t n_in, const int32_t* in_slots, const int32_t* frame_pos,
-              int32_t n_out, const int32_t* out_slots, lf::RopeArgs* A) {
+              int32_t n_out, const int32_t* out_slots, RopeCall* A) {
   if (r == nullptr) return LF_ERR_INVALID_ARG;
   if (r->d != 64 && r->d != 128) return LF_ERR_UNSUPPORTED;
   if (r->H < 1 || r->n_frames < 1 || r->height < 1 || r->width < 1 || r->pairs_t < 0 ||
@@ -660,25 +662,42 @@ bool slots_distinct(const int32_t* a, int na, const int32_t* b, int nb) {
   return true;
 }
 
-size_t rope_smem(const lf::RopeArgs& A, bool bwd) {
+size_t rope_smem(const lf::RopeHead& A, bool bwd) {
   return (size_t)A.groups * (A.d / 2) * sizeof(float2) + 32 * sizeof(float) +
          (bwd ? (size_t)(A.norm == LF_NORM_TOKEN ? A.H * A.d : A.d) * sizeof(float) : 0);
 }
 
-int launch_rope(const lf::RopeArgs& A, cudaStream_t st) {
+// The same call with room for few frames.
+lf::RopeArgs<lf::kRopeFewFrames> few_frames(const RopeCall& A, int n) {
+  lf::RopeArgs<lf::kRopeFewFrames> B;
+  static_cast<lf::RopeHead&>(B) = A;
+  for (int f = 0; f < n; ++f) {
+    B.pos[f] = A.pos[f];
+    B.x_slot[f] = A.x_slot[f];
+    B.dout_slot[f] = A.dout_slot[f];
+    B.out_slot[f] = A.out_slot[f];
+  }
+  return B;
+}
+
+template <int NF>
+int launch_rope_nf(const lf::RopeArgs<NF>& A, cudaStream_t st) {
   const int64_t grid = (A.n_tokens + A.groups - 1) / A.groups;
   if (grid > INT32_MAX) return LF_ERR_UNSUPPORTED;
   const int u = lf::cdiv(A.units, A.tpt);
-  auto kern = u == 1 ? lf::rope_kernel<1> : u == 2 ? lf::rope_kernel<2> : lf::rope_kernel<3>;
+  auto kern = u == 1 ? lf::rope_kernel<1, NF> : u == 2 ? lf::rope_kernel<2, NF> : lf::rope_kernel<3, NF>;
   kern<<<(unsigned)grid, A.tpt * A.groups, rope_smem(A, false), st>>>(A);
   return cuda_status(cudaGetLastError());
 }
 
-int launch_rope_bwd(const lf::RopeArgs& A, float* dweight, cudaStream_t st) {
+template <int NF>
+int launch_rope_bwd_nf(const lf::RopeArgs<NF>& A, float* dweight, cudaStream_t st) {
   const int u = lf::cdiv(A.units, A.tpt);
-  auto kern = u == 1 ? lf::rope_bwd_kernel<1> : u == 2 ? lf::rope_bwd_kernel<2> : lf::rope_bwd_kernel<3>;
+  auto kern = u == 1 ? lf::rope_bwd_kernel<1, NF>
+              : u == 2 ? lf::rope_bwd_kernel<2, NF> : lf::rope_bwd_kernel<3, NF>;
   const size_t smem = rope_smem(A, true);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LF_ERR_CUDA;
   const int64_t steps = (A.n_tokens + A.groups - 1) / A.groups;
   const int grid = (int)std::min<int64_t>(steps, lf::kRopeBwdCtas);
@@ -686,6 +705,16 @@ int launch_rope_bwd(const lf::RopeArgs& A, float* dweight, cudaStream_t st) {
   kern<<<grid, A.tpt * A.groups, smem, st>>>(A);
   lf::rope_dweight_kernel<<<lf::cdiv(n_dw, 32), 512, 0, st>>>(A.part, grid, n_dw, dweight);
   return cuda_status(cudaGetLastError());
+}
+
+int launch_rope(const RopeCall& A, int n_frames, cudaStream_t st) {
+  return n_frames <= lf::kRopeFewFrames ? launch_rope_nf(few_frames(A, n_frames), st)
+                                        : launch_rope_nf(A, st);
+}
+
+int launch_rope_bwd(const RopeCall& A, int n_frames, float* dweight, cudaStream_t st) {
+  return n_frames <= lf::kRopeFewFrames ? launch_rope_bwd_nf(few_frames(A, n_frames), dweight, st)
+                                        : launch_rope_bwd_nf(A, dweight, st);
 }
 
 // ---------------------------------------------------------------- fixed scratch
@@ -965,7 +994,7 @@ int lf_block_sparse_attn_backward(const lf_shape* shape, const void* q, const vo
 int lf_rope_frames(const lf_rope* rope, const void* x, int64_t x_stride, int32_t n_in,
                    const int32_t* in_slots, const int32_t* frame_pos, const float* weight,
                    void* out, int32_t n_out, const int32_t* out_slots, cudaStream_t stream) {
-  lf::RopeArgs A;
+  RopeCall A;
   memset(&A, 0, sizeof(A));
   int rc = make_rope(rope, n_in, in_slots, frame_pos, n_out, out_slots, &A);
   if (rc != LF_OK) return rc;
@@ -979,11 +1008,11 @@ int lf_rope_frames(const lf_rope* rope, const void* x, int64_t x_stride, int32_t
   A.weight = weight;
   A.out = static_cast<__nv_bfloat16*>(out);
   A.out_stride = (int64_t)A.H * A.d;
-  return launch_rope(A, stream);
+  return launch_rope(A, rope->n_frames, stream);
 }
 
 size_t lf_rope_backward_workspace_size(const lf_rope* rope) {
-  lf::RopeArgs A;
+  RopeCall A;
   if (rope == nullptr || make_rope(rope, rope->n_frames, nullptr, nullptr, rope->n_frames, nullptr,
                                    &A) != LF_OK || A.norm == LF_NORM_NONE)
     return 0;
@@ -997,7 +1026,7 @@ int lf_rope_frames_backward(const lf_rope* rope, const void* x, int64_t x_stride
                             const int32_t* out_slots, void* dx, int64_t dx_stride,
                             float* dweight, void* workspace, size_t workspace_bytes,
                             cudaStream_t stream) {
-  lf::RopeArgs A;
+  RopeCall A;
   memset(&A, 0, sizeof(A));
   int rc = make_rope(rope, n_in, in_slots, frame_pos, n_out, out_slots, &A);
   if (rc != LF_OK) return rc;
@@ -1020,7 +1049,7 @@ int lf_rope_frames_backward(const lf_rope* rope, const void* x, int64_t x_stride
     std::swap(A.x_slot, A.out_slot);
     A.x = static_cast<const __nv_bfloat16*>(dout);
     A.x_stride = row;
-    return launch_rope(A, stream);
+    return launch_rope(A, rope->n_frames, stream);
   }
   if (workspace == nullptr || !aligned(workspace, 256) ||
       workspace_bytes < lf_rope_backward_workspace_size(rope))
@@ -1033,7 +1062,7 @@ int lf_rope_frames_backward(const lf_rope* rope, const void* x, int64_t x_stride
   A.dout_stride = row;
   A.weight = weight;
   A.part = static_cast<float*>(workspace);
-  return launch_rope_bwd(A, dweight, stream);
+  return launch_rope_bwd(A, rope->n_frames, dweight, stream);
 }
 
 int lf_quantize_e4m3(const void* x, int64_t rows, int32_t H, int32_t d, const float* head_scale,

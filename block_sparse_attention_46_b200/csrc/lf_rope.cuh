@@ -26,7 +26,7 @@ constexpr int kRopeThreads = 256;            // per CTA, at most; a token's thre
 static_assert(kRopeUnits * 16 * kRopeThreads == LF_MAX_ROPE_CHANNELS, "the widest token");
 constexpr int kRopeBwdCtas = 296;            // backward with a norm: CTAs (partial sums of dw), at most
 
-struct RopeArgs {
+struct RopeHead {
   const __nv_bfloat16* x;      // rows of H * d channels, x_stride elements apart
   const __nv_bfloat16* dout;   // backward
   const float* weight;         // [d] (norm per head), [H * d] (per token) or null
@@ -42,8 +42,15 @@ struct RopeArgs {
   int p_t, p_h, p_w;           // ends of the three axes' pairs; pairs from p_w on are not turned
   float eps, inv_n, sign;      // sign: +1 turns by theta, -1 by -theta
   double turns[kRopeMaxPairs];             // frequency / 2 pi
-  int32_t pos[LF_MAX_FRAMES], x_slot[LF_MAX_FRAMES], dout_slot[LF_MAX_FRAMES],
-      out_slot[LF_MAX_FRAMES];
+};
+
+// Frames by value: up to kRopeFewFrames in 1.2 KB of kernel arguments, up to LF_MAX_FRAMES in
+// 4.7 KB, which cost a launch about 2 us more.
+constexpr int kRopeFewFrames = 32;
+
+template <int NF>
+struct RopeArgs : RopeHead {
+  int32_t pos[NF], x_slot[NF], dout_slot[NF], out_slot[NF];
 };
 
 // A unit's 16 channels as 32-bit values: pairs (v[2j], v[2j + 1]) when adjacent,
@@ -91,8 +98,8 @@ __device__ __forceinline__ void rope_turn(float* v, const float2* cs, int o, int
 }
 
 // (cos, sin) of every pair of the token at frame f, offset t, by the token's threads.
-__device__ __forceinline__ void rope_angles(const RopeArgs& A, int f, int t, int lane_t,
-                                            float2* cs) {
+template <typename Args>
+__device__ __forceinline__ void rope_angles(const Args& A, int f, int t, int lane_t, float2* cs) {
   const int row = t / A.width, col = t - row * A.width;
   for (int p = lane_t; p < A.d / 2; p += A.tpt) {
     float2 v = make_float2(1.f, 0.f);
@@ -116,7 +123,7 @@ __device__ __forceinline__ float rope_lane_sum(float v, int lo, int hi) {
 
 // Sum over a token's threads: lanes, then (wide tokens) its warps in order.  Every thread of
 // the CTA calls it.
-__device__ __forceinline__ float rope_token_sum(const RopeArgs& A, float v, float* s_warp) {
+__device__ __forceinline__ float rope_token_sum(const RopeHead& A, float v, float* s_warp) {
   v = rope_lane_sum(v, 1, A.tpt < 32 ? A.tpt : 32);
   if (A.tpt <= 32) return v;
   const int warp = threadIdx.x >> 5, wpt = A.tpt / 32, first = warp / wpt * wpt;
@@ -128,9 +135,9 @@ __device__ __forceinline__ float rope_token_sum(const RopeArgs& A, float v, floa
   return s;
 }
 
-template <int U>
+template <int U, int NF>
 __global__ void __launch_bounds__(kRopeThreads)
-rope_kernel(const __grid_constant__ RopeArgs A) {
+rope_kernel(const __grid_constant__ RopeArgs<NF> A) {
   extern __shared__ float2 s_cs[];                       // [groups][d / 2], then the warp sums
   float* s_warp = reinterpret_cast<float*>(s_cs + A.groups * (A.d / 2));
   const int grp = threadIdx.x / A.tpt, lane_t = threadIdx.x - grp * A.tpt;
@@ -198,9 +205,9 @@ rope_kernel(const __grid_constant__ RopeArgs A) {
 // in order and keeps its part of dw in registers; the parts of its warps are added in warp
 // order, those of the CTAs in CTA order by rope_dweight_kernel, so dw does not depend on
 // timing.
-template <int U>
+template <int U, int NF>
 __global__ void __launch_bounds__(kRopeThreads)
-rope_bwd_kernel(const __grid_constant__ RopeArgs A) {
+rope_bwd_kernel(const __grid_constant__ RopeArgs<NF> A) {
   extern __shared__ float2 s_cs[];
   float* s_warp = reinterpret_cast<float*>(s_cs + A.groups * (A.d / 2));
   float* s_dw = s_warp + 32;                             // [d or H * d]
