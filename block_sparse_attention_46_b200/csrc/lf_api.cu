@@ -496,7 +496,7 @@ int check_bwd_dims(const Dims& D) {
   const lf::KeyTiles K = lf::key_tiles(D, true);
   const long long tiles = (long long)K.n_dense + K.n_sink + (long long)K.n_list();
   const long long rows = (long long)D.nqb * D.B + 128;
-  if ((tiles + lf::tile_count(D)) * D.H > INT32_MAX / 2 || rows > INT32_MAX / 2 || rows * D.H * (D.d / 8) > (1LL << 38) ||
+  if ((tiles + lf::tile_count(D)) * D.H > INT32_MAX / 2 || rows > INT32_MAX / 32 ||
       (long long)D.H * D.nqb * (D.nsel + D.kc) > INT32_MAX / 2 || D.H > 65535)
     return LF_ERR_UNSUPPORTED;
   return LF_OK;
@@ -531,15 +531,15 @@ int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
   const bool cache_grad = b.dk_cache != nullptr;
   lf::BwdRows rows = w.rows;
   const lf::KeyTiles K = lf::key_tiles(D, cache_grad);
-  {
-    const long long items = ((long long)D.nqb * D.B + lf::bwd_dense_boxes(D) * 64 - D.ncur) * D.H;
-    const long long threads = items * (D.d / 8);
-    lf::bwd_rows_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
-        static_cast<const __nv_bfloat16*>(b.out), static_cast<const __nv_bfloat16*>(b.dout), b.lse,
-        rows, w.inv_total, lf::key_tiles(D, true).n_list() > 0, D);
-  }
-  lf::plan_kernel<<<dim3(lf::cdiv(lf::tile_count(D), lf::kPlanWarps), D.H), lf::kPlanWarps * 32, 0, st>>>(
-      D.F > 0 ? block_idx : nullptr, D.kc > 0 ? cur_idx : nullptr, w.attn.plan, w.attn.plan_cnt, D);
+  const int plan_ctas = lf::cdiv(lf::tile_count(D), lf::kPlanWarps);
+  const int padded = D.nqb * D.B + lf::bwd_dense_boxes(D) * 64 - D.ncur;
+  const int row_ctas = lf::cdiv(padded, lf::kPrepThreads / (D.d / 8));
+  const int longest = D.nsel > D.kc ? D.nsel : D.kc;
+  lf::bwd_prep_kernel<<<dim3(plan_ctas + row_ctas, D.H), lf::kPrepThreads,
+                        lf::kPlanWarps * 2 * longest * sizeof(int32_t), st>>>(
+      static_cast<const __nv_bfloat16*>(b.out), static_cast<const __nv_bfloat16*>(b.dout), b.lse, rows,
+      lf::key_tiles(D, true).n_list() > 0, D.F > 0 ? block_idx : nullptr, D.kc > 0 ? cur_idx : nullptr,
+      w.attn.plan, w.attn.plan_cnt, w.inv_total, plan_ctas, longest, D);
   if (K.n_list() > 0)
     lf::bwd_transpose_kernel<<<lf::cdiv(K.n_list() * D.H, lf::kInvWarps), lf::kInvWarps * 32, 0, st>>>(
         w.attn.plan, w.attn.plan_cnt, K, w.inv, w.inv_total, w.inv_off, w.inv_cnt, D);
@@ -616,7 +616,7 @@ int make_rope(const lf_rope* r, int32_t n_in, const int32_t* in_slots, const int
   A->d = r->d;
   A->T = r->height * r->width;
   A->width = r->width;
-  A->n_tokens = (int64_t)r->n_frames * A->T;
+  A->n_frames = r->n_frames;
   if ((int64_t)(n_in > n_out ? n_in : n_out) * A->T > ((int64_t)1 << 40) / (r->H * r->d))
     return LF_ERR_UNSUPPORTED;
   int rc;
@@ -643,12 +643,12 @@ int make_rope(const lf_rope* r, int32_t n_in, const int32_t* in_slots, const int
   A->upd = r->d / 16;
   A->units = r->H * A->upd;
   // threads per token: the fewest lanes (a power of two, whole heads) that hold it in one
-  // unit each, else a warp with up to kRopeUnits units per lane, else several warps
+  // unit each, else whole warps with as few units per thread as a CTA's threads allow
   if (A->units <= 32) {
     A->tpt = A->upd;
     while (A->tpt < A->units) A->tpt *= 2;
   } else {
-    A->tpt = 32 * lf::cdiv(A->units, 32 * lf::kRopeUnits);
+    A->tpt = 32 * lf::cdiv(A->units, 32 * lf::cdiv(A->units, lf::kRopeThreads));
   }
   A->groups = lf::kRopeThreads / A->tpt;
   return LF_OK;
@@ -662,9 +662,11 @@ bool slots_distinct(const int32_t* a, int na, const int32_t* b, int nb) {
   return true;
 }
 
-size_t rope_smem(const lf::RopeHead& A, bool bwd) {
-  return (size_t)A.groups * (A.d / 2) * sizeof(float2) + 32 * sizeof(float) +
-         (bwd ? (size_t)(A.norm == LF_NORM_TOKEN ? A.H * A.d : A.d) * sizeof(float) : 0);
+size_t rope_smem(const lf::RopeHead& A, bool bwd, int nt = 1) {
+  const size_t angles = (size_t)A.groups * (A.d / 2) * sizeof(float2);
+  if (!bwd) return nt * (angles + (lf::kRopeThreads / 32) * sizeof(float));
+  return 2 * angles + 2 * (lf::kRopeThreads / 32) * sizeof(float2) +
+         (size_t)(A.norm == LF_NORM_TOKEN ? A.H * A.d : A.d) * sizeof(float);
 }
 
 // The same call with room for few frames.
@@ -682,11 +684,15 @@ lf::RopeArgs<lf::kRopeFewFrames> few_frames(const RopeCall& A, int n) {
 
 template <int NF>
 int launch_rope_nf(const lf::RopeArgs<NF>& A, cudaStream_t st) {
-  const int64_t grid = (A.n_tokens + A.groups - 1) / A.groups;
-  if (grid > INT32_MAX) return LF_ERR_UNSUPPORTED;
   const int u = lf::cdiv(A.units, A.tpt);
-  auto kern = u == 1 ? lf::rope_kernel<1, NF> : u == 2 ? lf::rope_kernel<2, NF> : lf::rope_kernel<3, NF>;
-  kern<<<(unsigned)grid, A.tpt * A.groups, rope_smem(A, false), st>>>(A);
+  const int nt = u == 1 && rope_smem(A, false, lf::kRopeTokens) <= 48 * 1024 &&
+                 (int64_t)A.n_frames * lf::cdiv(A.T, A.groups) >= lf::kRopeManyGroups
+                     ? lf::kRopeTokens : 1;
+  auto kern = nt > 1   ? lf::rope_kernel<1, lf::kRopeTokens, NF>
+              : u == 1 ? lf::rope_kernel<1, 1, NF>
+              : u == 2 ? lf::rope_kernel<2, 1, NF> : lf::rope_kernel<3, 1, NF>;
+  const dim3 grid(lf::cdiv(A.T, A.groups * nt), A.n_frames), block(A.tpt, A.groups);
+  kern<<<grid, block, rope_smem(A, false, nt), st>>>(A);
   return cuda_status(cudaGetLastError());
 }
 
@@ -699,10 +705,10 @@ int launch_rope_bwd_nf(const lf::RopeArgs<NF>& A, float* dweight, cudaStream_t s
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LF_ERR_CUDA;
-  const int64_t steps = (A.n_tokens + A.groups - 1) / A.groups;
+  const int64_t steps = (int64_t)lf::cdiv(A.T, A.groups) * A.n_frames;
   const int grid = (int)std::min<int64_t>(steps, lf::kRopeBwdCtas);
   const int n_dw = A.norm == LF_NORM_TOKEN ? A.H * A.d : A.d;
-  kern<<<grid, A.tpt * A.groups, smem, st>>>(A);
+  kern<<<grid, dim3(A.tpt, A.groups), smem, st>>>(A);
   lf::rope_dweight_kernel<<<lf::cdiv(n_dw, 32), 512, 0, st>>>(A.part, grid, n_dw, dweight);
   return cuda_status(cudaGetLastError());
 }

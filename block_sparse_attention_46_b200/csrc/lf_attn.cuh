@@ -134,20 +134,16 @@ __device__ __forceinline__ bool warp_stage_lists(const int32_t* lists, int n, in
 
 constexpr int kPlanWarps = 4;
 
-// Key plan of each (query tile, head), one warp: sink blocks (kept by both query blocks),
+// Key plan of query tile t of head h, one warp: sink blocks (kept by both query blocks),
 // then the union of the query blocks' current-chunk lists (when the current chunk is
 // sparse), then the union of their history lists.  A list that fails validation is
 // dropped and LF_ERR_BAD_INDEX recorded.
-__global__ void __launch_bounds__(kPlanWarps * 32)
-plan_kernel(const int32_t* __restrict__ block_idx, const int32_t* __restrict__ cur_idx,
-            uint32_t* __restrict__ plan, int32_t* __restrict__ plan_cnt, const Dims D) {
-  __shared__ int32_t s_ab[kPlanWarps][2][LF_MAX_SELECTED];
+__device__ __forceinline__ void plan_tile(const int32_t* __restrict__ block_idx,
+                                          const int32_t* __restrict__ cur_idx,
+                                          uint32_t* __restrict__ plan, int32_t* __restrict__ plan_cnt,
+                                          int t, int h, int32_t* sa, int32_t* sb, const Dims& D) {
   const int ntiles = tile_count(D);
-  const int t = blockIdx.x * kPlanWarps + (threadIdx.x >> 5), h = blockIdx.y;
   const int lane = threadIdx.x & 31;
-  if (t >= ntiles) return;
-  int32_t* sa = s_ab[threadIdx.x >> 5][0];
-  int32_t* sb = s_ab[threadIdx.x >> 5][1];
   uint32_t* out = plan + ((size_t)h * ntiles + t) * plan_stride(D);
   const int qa = D.B == 64 ? 2 * t : t;
   const int qbB = (D.B == 64 && 2 * t + 1 < D.nqb) ? 2 * t + 1 : -1;
@@ -172,6 +168,16 @@ plan_kernel(const int32_t* __restrict__ block_idx, const int32_t* __restrict__ c
     if (bad) record_status(LF_ERR_BAD_INDEX);
     plan_cnt[(size_t)h * ntiles + t] = cnt;
   }
+}
+
+__global__ void __launch_bounds__(kPlanWarps * 32)
+plan_kernel(const int32_t* __restrict__ block_idx, const int32_t* __restrict__ cur_idx,
+            uint32_t* __restrict__ plan, int32_t* __restrict__ plan_cnt, const Dims D) {
+  __shared__ int32_t s_ab[kPlanWarps][2][LF_MAX_SELECTED];
+  const int t = blockIdx.x * kPlanWarps + (threadIdx.x >> 5);
+  if (t >= tile_count(D)) return;
+  plan_tile(block_idx, cur_idx, plan, plan_cnt, t, blockIdx.y, s_ab[threadIdx.x >> 5][0],
+            s_ab[threadIdx.x >> 5][1], D);
 }
 
 

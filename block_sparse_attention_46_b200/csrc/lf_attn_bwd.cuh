@@ -22,6 +22,8 @@ namespace lf {
 // ---------------------------------------------------------------------------------
 constexpr int kBoxFloats = 128;
 
+static_assert(kPlanWarps * 32 == kBoxFloats, "one thread per value of the padding box");
+
 struct BwdRows {
   float *dense, *blk;
 };
@@ -29,26 +31,40 @@ struct BwdRows {
 __host__ __device__ inline int bwd_dense_boxes(const Dims& D) { return cdiv(D.ncur, 128) * 2; }
 __host__ __device__ inline int bwd_blk_boxes(const Dims& D) { return D.nqb * (D.B / 64); }
 
-// d / 8 threads per (row, head), 16-byte loads, heads fastest (a token's row is contiguous).
-// Also zeroes the entry counter of the transposed plans.
-__global__ void __launch_bounds__(256)
-bwd_rows_kernel(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ dout,
-                const float* __restrict__ lse, BwdRows R, int32_t* inv_total, bool blk,
-                const Dims D) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) *inv_total = 0;
-  if (blk && blockIdx.x == 0 && threadIdx.x < kBoxFloats)
-    R.blk[(size_t)D.H * bwd_blk_boxes(D) * kBoxFloats + threadIdx.x] =
-        threadIdx.x < 64 ? -INFINITY : 0.f;
-  const int per = D.d / 8;
-  const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long item = idx / per;
-  const int part = (int)(idx % per);
+// What the two passes start from, in one launch (apart, the plans' 10 us of latency on the 480p
+// chunk came on top of the rows' 13): per head (grid.y) the first plan_ctas CTAs make key plans,
+// a warp each, the others the row values with d / 8 threads per row and 16-byte loads.  Also
+// zeroes the entry counter of the transposed plans.
+constexpr int kPrepThreads = kPlanWarps * 32;
+
+__global__ void __launch_bounds__(kPrepThreads)
+bwd_prep_kernel(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ dout,
+                const float* __restrict__ lse, BwdRows R, bool blk,
+                const int32_t* __restrict__ block_idx, const int32_t* __restrict__ cur_idx,
+                uint32_t* __restrict__ plan, int32_t* __restrict__ plan_cnt, int32_t* inv_total,
+                int plan_ctas, int longest, const Dims D) {
+  extern __shared__ int32_t s_lists[];                 // two lists per warp
+  if ((int)blockIdx.x < plan_ctas) {
+    const int w = threadIdx.x >> 5, t = blockIdx.x * kPlanWarps + w;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+      if (threadIdx.x == 0) *inv_total = 0;
+      if (blk)                                         // the box of padding
+        R.blk[(size_t)D.H * bwd_blk_boxes(D) * kBoxFloats + threadIdx.x] =
+            threadIdx.x < 64 ? -INFINITY : 0.f;
+    }
+    if (t < tile_count(D))
+      plan_tile(block_idx, cur_idx, plan, plan_cnt, t, blockIdx.y, s_lists + 2 * w * longest,
+                s_lists + (2 * w + 1) * longest, D);
+    return;
+  }
+  const int lg = D.d == 128 ? 4 : 3, per = 1 << lg;      // threads per row
+  const int p = ((blockIdx.x - plan_ctas) * kPrepThreads + threadIdx.x) >> lg;
+  const int part = threadIdx.x & (per - 1), h = blockIdx.y;
   const int blk_rows = D.nqb * D.B, dense_rows = bwd_dense_boxes(D) * 64;
-  const long long p = item / D.H;                        // padded row; then the dense padding
-  const int h = (int)(item % D.H);
+  // p: padded row; then the dense padding
   int tok = -1;
   if (p < blk_rows) {
-    const int qb = (int)p / D.B, i = (int)p % D.B;
+    const int qb = p / D.B, i = p % D.B;
     if (i < block_len(D, qb % D.nbpf)) tok = (qb / D.nbpf) * D.T + (qb % D.nbpf) * D.B + i;
   }
   float s = 0.f;
@@ -76,10 +92,10 @@ bwd_rows_kernel(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __re
     b[64] = -s;
   };
   if (p < blk_rows) {
-    if (blk) put(R.blk, (size_t)h * bwd_blk_boxes(D), (int)p);
+    if (blk) put(R.blk, (size_t)h * bwd_blk_boxes(D), p);
     if (tok >= 0) put(R.dense, (size_t)h * bwd_dense_boxes(D), tok);
   } else if (p - blk_rows < dense_rows - D.ncur) {
-    put(R.dense, (size_t)h * bwd_dense_boxes(D), D.ncur + (int)(p - blk_rows));
+    put(R.dense, (size_t)h * bwd_dense_boxes(D), D.ncur + p - blk_rows);
   }
 }
 

@@ -10,8 +10,10 @@
 // Everything is bound by HBM: 4 bytes per element forward, 6 backward with a norm.  A token
 // is held in the registers of `tpt` threads (4 to 32 lanes of a warp, or several warps for
 // wide tokens), 16 channels (two 16-byte loads) per unit and up to kRopeUnits units per
-// thread, so x is read once although the norm needs a sum over it first.  A unit holds whole
-// pairs: 16 adjacent channels, or 8 from each half of the head.  Each token's d / 2 angles
+// thread, so x is read once although the norm needs a sum over it first.  A unit is 8 channels
+// of each half of its head: whole pairs in either pairing, and every load and store of a warp
+// covers whole 128-byte lines (as 16 adjacent channels per thread, in two pieces, 24 cached
+// frames of 12 x 128 channels took 54 us instead of 43).  Each token's d / 2 angles
 // are computed once by its threads and shared: position * frequency in turns in 64 bits,
 // reduced to [-1/2, 1/2] there, then sine and cosine in 32 bits, so the angle's error does
 // not grow with the position (a 32-bit product would be off by 2^-24 of it).
@@ -24,6 +26,10 @@ constexpr int kRopeMaxPairs = 64;            // d / 2
 constexpr int kRopeUnits = 3;                // 16-channel units per thread, at most
 constexpr int kRopeThreads = 256;            // per CTA, at most; a token's threads are in one CTA
 static_assert(kRopeUnits * 16 * kRopeThreads == LF_MAX_ROPE_CHANNELS, "the widest token");
+// Forward, wide tokens: tokens per thread where there are this many groups of threads for
+// them (24 cached frames: 43 us against 45 with one token each, the 480p queries 15.7
+// against 17.5); below, one, for the latency of small calls.
+constexpr int kRopeTokens = 4, kRopeManyGroups = 2000;
 constexpr int kRopeBwdCtas = 296;            // backward with a norm: CTAs (partial sums of dw), at most
 
 struct RopeHead {
@@ -33,8 +39,7 @@ struct RopeHead {
   __nv_bfloat16* out;          // forward: y; backward: dx
   float* part;                 // backward: [CTAs, d or H * d] partial sums of dw
   int64_t x_stride, dout_stride, out_stride;
-  int64_t n_tokens;
-  int H, d, T, width;
+  int H, d, T, width, n_frames;
   int units;                   // H * d / 16
   int tpt, groups;             // threads per token, tokens per CTA at a time
   int upd;                     // units per head, d / 16
@@ -76,11 +81,12 @@ __device__ __forceinline__ uint4 rope_pack(const float* v) {
 
 // Turns a unit's eight pairs; cs holds (cos, sin) of the head's pairs, o is the unit's
 // index in its head.
-__device__ __forceinline__ void rope_turn(float* v, const float2* cs, int o, int halves) {
-  const float4* c4 = reinterpret_cast<const float4*>(cs + o * 8);
+__device__ __forceinline__ void rope_turn(float* v, const float2* cs, int o, int quarter, int halves) {
+  const float4* c4 = reinterpret_cast<const float4*>(cs + o * (halves ? 8 : 4));
+  const float4* c4b = reinterpret_cast<const float4*>(cs + (halves ? o * 8 + 4 : quarter + o * 4));
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float4 c = c4[j];
+    const float4 c = j < 2 ? c4[j] : c4b[j - 2];
     if (halves) {
       const float a0 = v[2 * j], b0 = v[8 + 2 * j], a1 = v[2 * j + 1], b1 = v[8 + 2 * j + 1];
       v[2 * j] = a0 * c.x - b0 * c.y;
@@ -121,163 +127,176 @@ __device__ __forceinline__ float rope_lane_sum(float v, int lo, int hi) {
   return v;
 }
 
-// Sum over a token's threads: lanes, then (wide tokens) its warps in order.  Every thread of
-// the CTA calls it.
-__device__ __forceinline__ float rope_token_sum(const RopeHead& A, float v, float* s_warp) {
-  v = rope_lane_sum(v, 1, A.tpt < 32 ? A.tpt : 32);
-  if (A.tpt <= 32) return v;
-  const int warp = threadIdx.x >> 5, wpt = A.tpt / 32, first = warp / wpt * wpt;
-  __syncthreads();                       // the previous sum has been read
-  if ((threadIdx.x & 31) == 0) s_warp[warp] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < wpt; ++i) s += s_warp[first + i];
-  return s;
-}
-
-template <int U, int NF>
+// A CTA is tpt x groups threads: x within the token, y the group of NT successive tokens, all
+// loaded before the first is worked on.  grid.y: frames.
+template <int U, int NT, int NF>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const __grid_constant__ RopeArgs<NF> A) {
-  extern __shared__ float2 s_cs[];                       // [groups][d / 2], then the warp sums
-  float* s_warp = reinterpret_cast<float*>(s_cs + A.groups * (A.d / 2));
-  const int grp = threadIdx.x / A.tpt, lane_t = threadIdx.x - grp * A.tpt;
-  const int64_t tok = (int64_t)blockIdx.x * A.groups + grp;
-  const bool live = tok < A.n_tokens;
-  const int f = live ? (int)(tok / A.T) : 0, t = live ? (int)(tok - (int64_t)f * A.T) : 0;
-  const int o = lane_t % A.upd;
-  const int ca = A.halves ? o * 8 : o * 16, cb = A.halves ? A.d / 2 + o * 8 : o * 16 + 8;
-  const __nv_bfloat16* xr = A.x + ((int64_t)A.x_slot[f] * A.T + t) * A.x_stride;
-  uint4 a[U], b[U];
+  extern __shared__ float2 s_cs[];                       // [groups][NT][d / 2], then the warp sums
+  float* s_warp = reinterpret_cast<float*>(s_cs + A.groups * NT * (A.d / 2));   // [NT][warps]
+  const int grp = threadIdx.y, lane_t = threadIdx.x;
+  const int f = blockIdx.y, t0 = (blockIdx.x * A.groups + grp) * NT;
+  const int o = lane_t & (A.upd - 1);                    // unit in its head (upd: 4 or 8)
+  const int ca = o * 8, cb = A.d / 2 + o * 8;            // the unit's two pieces of its head
+  const __nv_bfloat16* xr = A.x + ((int64_t)A.x_slot[f] * A.T + t0) * A.x_stride;
+  uint4 a[NT][U], b[NT][U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int id = lane_t + u * A.tpt, base = id / A.upd * A.d;
-    a[u] = b[u] = make_uint4(0, 0, 0, 0);
-    if (live && id < A.units) {
-      a[u] = *reinterpret_cast<const uint4*>(xr + base + ca);
-      b[u] = *reinterpret_cast<const uint4*>(xr + base + cb);
-    }
-  }
-  float2* cs = s_cs + grp * (A.d / 2);
-  if (live) rope_angles(A, f, t, lane_t, cs);
-  __syncthreads();
-  float v[U][16], r[U];
-  float ss = 0.f;
+  for (int k = 0; k < NT; ++k)
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    rope_unpack(a[u], b[u], v[u]);
-    r[u] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[u] = fmaf(v[u][i], v[u][i], r[u]);
-    ss += r[u];
-  }
-  if (A.norm == LF_NORM_TOKEN) {
-    ss = rsqrtf(rope_token_sum(A, ss, s_warp) * A.inv_n + A.eps);
-#pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = ss;
-  } else if (A.norm == LF_NORM_HEAD) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = rsqrtf(rope_lane_sum(r[u], 1, A.upd) * A.inv_n + A.eps);
-  }
-  if (!live) return;
-  __nv_bfloat16* yr = A.out + ((int64_t)A.out_slot[f] * A.T + t) * A.out_stride;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int id = lane_t + u * A.tpt, base = id / A.upd * A.d;
-    if (id >= A.units) break;
-    if (A.norm != LF_NORM_NONE) {
-      const float* w = A.weight + (A.norm == LF_NORM_TOKEN ? base : 0);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 w4 = *reinterpret_cast<const float4*>(w + (q < 2 ? ca : cb) + (q & 1) * 4);
-        v[u][4 * q] *= r[u] * w4.x;
-        v[u][4 * q + 1] *= r[u] * w4.y;
-        v[u][4 * q + 2] *= r[u] * w4.z;
-        v[u][4 * q + 3] *= r[u] * w4.w;
+    for (int u = 0; u < U; ++u) {
+      const int id = lane_t + u * A.tpt, base = (id - o) * 16;   // 16 * upd = d channels a head
+      a[k][u] = b[k][u] = make_uint4(0, 0, 0, 0);
+      if (t0 + k < A.T && id < A.units) {
+        a[k][u] = *reinterpret_cast<const uint4*>(xr + k * A.x_stride + base + ca);
+        b[k][u] = *reinterpret_cast<const uint4*>(xr + k * A.x_stride + base + cb);
       }
     }
-    rope_turn(v[u], cs, o, A.halves);
-    *reinterpret_cast<uint4*>(yr + base + ca) = rope_pack(v[u]);
-    *reinterpret_cast<uint4*>(yr + base + cb) = rope_pack(v[u] + 8);
+  float2* cs = s_cs + grp * NT * (A.d / 2);
+  if (A.p_w > 0) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+      if (t0 + k < A.T) rope_angles(A, f, t0 + k, lane_t, cs + k * (A.d / 2));
+  }
+  float r[NT][U];
+  if (A.norm != LF_NORM_NONE) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      float ss = 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float v[16];
+        rope_unpack(a[k][u], b[k][u], v);
+        r[k][u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[k][u] = fmaf(v[i], v[i], r[k][u]);
+        if (A.norm == LF_NORM_HEAD)
+          r[k][u] = rsqrtf(rope_lane_sum(r[k][u], 1, A.upd) * A.inv_n + A.eps);
+        ss += r[k][u];
+      }
+      if (A.norm == LF_NORM_TOKEN) {
+        ss = rope_lane_sum(ss, 1, A.tpt < 32 ? A.tpt : 32);
+        if (A.tpt > 32 && (lane_t & 31) == 0)
+          s_warp[k * (kRopeThreads / 32) + ((grp * A.tpt + lane_t) >> 5)] = ss;
+        r[k][0] = ss;
+      }
+    }
+  }
+  __syncthreads();                                       // angles and warp sums
+  __nv_bfloat16* yr = A.out + ((int64_t)A.out_slot[f] * A.T + t0) * A.out_stride;
+#pragma unroll
+  for (int k = 0; k < NT; ++k) {
+    if (t0 + k >= A.T) return;
+    if (A.norm == LF_NORM_TOKEN) {
+      float ss = r[k][0];
+      if (A.tpt > 32) {
+        ss = 0.f;
+        for (int i = 0; i < A.tpt >> 5; ++i) ss += s_warp[k * (kRopeThreads / 32) + grp * (A.tpt >> 5) + i];
+      }
+      ss = rsqrtf(ss * A.inv_n + A.eps);
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[k][u] = ss;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int id = lane_t + u * A.tpt, base = (id - o) * 16;
+      if (id >= A.units) break;
+      float v[16];
+      rope_unpack(a[k][u], b[k][u], v);
+      if (A.norm != LF_NORM_NONE) {
+        const float* w = A.weight + (A.norm == LF_NORM_TOKEN ? base : 0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 w4 = *reinterpret_cast<const float4*>(w + (q < 2 ? ca : cb) + (q & 1) * 4);
+          v[4 * q] *= r[k][u] * w4.x;
+          v[4 * q + 1] *= r[k][u] * w4.y;
+          v[4 * q + 2] *= r[k][u] * w4.z;
+          v[4 * q + 3] *= r[k][u] * w4.w;
+        }
+      }
+      if (A.p_w > 0) rope_turn(v, cs + k * (A.d / 2), o, A.d / 4, A.halves);
+      *reinterpret_cast<uint4*>(yr + k * A.out_stride + base + ca) = rope_pack(v);
+      *reinterpret_cast<uint4*>(yr + k * A.out_stride + base + cb) = rope_pack(v + 8);
+    }
   }
 }
 
-// Gradient with a norm.  Each CTA walks tokens blockIdx.x, + gridDim.x, ... (groups of them)
-// in order and keeps its part of dw in registers; the parts of its warps are added in warp
-// order, those of the CTAs in CTA order by rope_dweight_kernel, so dw does not depend on
-// timing.
+// Gradient with a norm, both of its sums over channels in one pass: with m = mean(w g x),
+//   dx = r w g - r^3 m x,  dw += g x r.
+// Each CTA walks steps blockIdx.x, + gridDim.x, ... (`groups` tokens of a frame each) in order,
+// loading the next step's channels while it works on this one's, and keeps its part of dw in
+// registers; the parts of its warps are added in warp order, those of the CTAs in a fixed
+// order by rope_dweight_kernel, so dw does not depend on timing.  Angles and warp sums have
+// two buffers, which leaves two barriers per step.
 template <int U, int NF>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_bwd_kernel(const __grid_constant__ RopeArgs<NF> A) {
-  extern __shared__ float2 s_cs[];
-  float* s_warp = reinterpret_cast<float*>(s_cs + A.groups * (A.d / 2));
-  float* s_dw = s_warp + 32;                             // [d or H * d]
-  const int grp = threadIdx.x / A.tpt, lane_t = threadIdx.x - grp * A.tpt;
-  const int o = lane_t % A.upd;
-  const int ca = A.halves ? o * 8 : o * 16, cb = A.halves ? A.d / 2 + o * 8 : o * 16 + 8;
-  float2* cs = s_cs + grp * (A.d / 2);
+  extern __shared__ float2 s_cs[];                       // [2][groups][d / 2]
+  const int cs_len = A.groups * (A.d / 2);
+  float2* s_warp = s_cs + 2 * cs_len;                    // [2][warps] sums of x^2 and of w g x
+  float* s_dw = reinterpret_cast<float*>(s_warp + 2 * (kRopeThreads / 32));   // [d or H * d]
+  const int grp = threadIdx.y, lane_t = threadIdx.x, tid = grp * A.tpt + lane_t;
+  const int o = lane_t & (A.upd - 1);
+  const int ca = o * 8, cb = A.d / 2 + o * 8;            // the unit's two pieces of its head
   const bool per_token = A.norm == LF_NORM_TOKEN;
+  const int wpt = A.tpt >> 5;                            // warps per token, 0: lanes of one
   float dw[U][16];
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < 16; ++i) dw[u][i] = 0.f;
 
-  const int64_t n_steps = (A.n_tokens + A.groups - 1) / A.groups;
-  for (int64_t step = blockIdx.x; step < n_steps; step += gridDim.x) {
-    const int64_t tok = step * A.groups + grp;
-    const bool live = tok < A.n_tokens;
-    const int f = live ? (int)(tok / A.T) : 0, t = live ? (int)(tok - (int64_t)f * A.T) : 0;
+  const int per_frame = (A.T + A.groups - 1) / A.groups;
+  struct Place { int f, i; };                            // frame and step in it
+  auto advance = [&](Place p, int n) {
+    p.i += n;
+    while (p.f < A.n_frames && p.i >= per_frame) p.i -= per_frame, ++p.f;
+    return p;
+  };
+  uint4 nxa[U], nxb[U], nga[U], ngb[U];
+  auto load = [&](Place p) {
+    const int t = p.i * A.groups + grp;
+    const bool live = p.f < A.n_frames && t < A.T;
+    const int f = p.f < A.n_frames ? p.f : 0;
     const __nv_bfloat16* xr = A.x + ((int64_t)A.x_slot[f] * A.T + t) * A.x_stride;
     const __nv_bfloat16* gr = A.dout + ((int64_t)A.dout_slot[f] * A.T + t) * A.dout_stride;
-    uint4 xa[U], xb[U], ga[U], gb[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int id = lane_t + u * A.tpt, base = id / A.upd * A.d;
-      xa[u] = xb[u] = ga[u] = gb[u] = make_uint4(0, 0, 0, 0);
+      const int id = lane_t + u * A.tpt, base = (id - o) * 16;
+      nxa[u] = nxb[u] = nga[u] = ngb[u] = make_uint4(0, 0, 0, 0);
       if (live && id < A.units) {
-        xa[u] = *reinterpret_cast<const uint4*>(xr + base + ca);
-        xb[u] = *reinterpret_cast<const uint4*>(xr + base + cb);
-        ga[u] = *reinterpret_cast<const uint4*>(gr + base + ca);
-        gb[u] = *reinterpret_cast<const uint4*>(gr + base + cb);
+        nxa[u] = *reinterpret_cast<const uint4*>(xr + base + ca);
+        nxb[u] = *reinterpret_cast<const uint4*>(xr + base + cb);
+        nga[u] = *reinterpret_cast<const uint4*>(gr + base + ca);
+        ngb[u] = *reinterpret_cast<const uint4*>(gr + base + cb);
       }
     }
-    __syncthreads();                                     // the previous token's angles were read
-    if (live) rope_angles(A, f, t, lane_t, cs);
-    __syncthreads();
-    float r[U], c[U];
-    {
-      float ss = 0.f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float x[16];
-        rope_unpack(xa[u], xb[u], x);
-        r[u] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) r[u] = fmaf(x[i], x[i], r[u]);
-        ss += r[u];
-      }
-      if (per_token) {
-        ss = rsqrtf(rope_token_sum(A, ss, s_warp) * A.inv_n + A.eps);
-#pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = ss;
-      } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          r[u] = rsqrtf(rope_lane_sum(r[u], 1, A.upd) * A.inv_n + A.eps);
-      }
-    }
-    // c = mean(w g xn); dw += g xn
+  };
+  Place at = advance(Place{0, 0}, blockIdx.x);
+  load(at);
+  for (int buf = 0; at.f < A.n_frames; buf ^= 1) {
+    const int f = at.f, t = at.i * A.groups + grp;
+    const bool live = t < A.T;
+    float2* cs = s_cs + buf * cs_len + grp * (A.d / 2);
+    if (live && A.p_w > 0) rope_angles(A, f, t, lane_t, cs);
+    uint4 xa[U], xb[U];
     float g[U][16];
-    float cc = 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int id = lane_t + u * A.tpt, base = id / A.upd * A.d;
+      xa[u] = nxa[u], xb[u] = nxb[u];
+      rope_unpack(nga[u], ngb[u], g[u]);
+    }
+    at = advance(at, gridDim.x);
+    load(at);
+    __syncthreads();                                     // angles
+    float ss[U], m[U], ss_all = 0.f, m_all = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int id = lane_t + u * A.tpt, base = (id - o) * 16;
       float x[16];
       rope_unpack(xa[u], xb[u], x);
-      rope_unpack(ga[u], gb[u], g[u]);
-      c[u] = 0.f;
+      ss[u] = m[u] = 0.f;
       if (live && id < A.units) {
-        rope_turn(g[u], cs, o, A.halves);
+        if (A.p_w > 0) rope_turn(g[u], cs, o, A.d / 4, A.halves);
         const float* w = A.weight + (per_token ? base : 0);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -286,43 +305,66 @@ rope_bwd_kernel(const __grid_constant__ RopeArgs<NF> A) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int i = 4 * q + k;
-            const float gx = g[u][i] * (x[i] * r[u]);
-            dw[u][i] += gx;
-            c[u] = fmaf(wv[k], gx, c[u]);
-            g[u][i] *= wv[k];
+            ss[u] = fmaf(x[i], x[i], ss[u]);
+            m[u] = fmaf(wv[k], g[u][i] * x[i], m[u]);
           }
         }
       }
-      cc += c[u];
+      ss_all += ss[u];
+      m_all += m[u];
     }
     if (per_token) {
-      cc = rope_token_sum(A, cc, s_warp) * A.inv_n;
-#pragma unroll
-      for (int u = 0; u < U; ++u) c[u] = cc;
+      ss_all = rope_lane_sum(ss_all, 1, A.tpt < 32 ? A.tpt : 32);
+      m_all = rope_lane_sum(m_all, 1, A.tpt < 32 ? A.tpt : 32);
+      if (wpt > 1) {
+        float2* sw = s_warp + buf * (kRopeThreads / 32);
+        if ((lane_t & 31) == 0) sw[tid >> 5] = make_float2(ss_all, m_all);
+        __syncthreads();
+        ss_all = m_all = 0.f;
+        for (int i = 0; i < wpt; ++i) {
+          const float2 v = sw[grp * wpt + i];
+          ss_all += v.x;
+          m_all += v.y;
+        }
+      }
     } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u) c[u] = rope_lane_sum(c[u], 1, A.upd) * A.inv_n;
-    }
-    if (live) {
-      __nv_bfloat16* dr = A.out + ((int64_t)A.out_slot[f] * A.T + t) * A.out_stride;
-#pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int id = lane_t + u * A.tpt, base = id / A.upd * A.d;
-        if (id >= A.units) break;
-        float x[16];
-        rope_unpack(xa[u], xb[u], x);
-        const float rc = r[u] * r[u] * c[u];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = fmaf(r[u], g[u][i], -rc * x[i]);
-        *reinterpret_cast<uint4*>(dr + base + ca) = rope_pack(x);
-        *reinterpret_cast<uint4*>(dr + base + cb) = rope_pack(x + 8);
+        ss[u] = rope_lane_sum(ss[u], 1, A.upd);
+        m[u] = rope_lane_sum(m[u], 1, A.upd);
       }
+    }
+    if (!live) continue;                                 // (the same for a token's threads)
+    __nv_bfloat16* dr = A.out + ((int64_t)A.out_slot[f] * A.T + t) * A.out_stride;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int id = lane_t + u * A.tpt, base = (id - o) * 16;
+      if (id >= A.units) break;
+      if (!per_token) ss_all = ss[u], m_all = m[u];
+      const float r = rsqrtf(ss_all * A.inv_n + A.eps), c = r * r * r * (m_all * A.inv_n);
+      const float* w = A.weight + (per_token ? base : 0);
+      float x[16];
+      rope_unpack(xa[u], xb[u], x);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 w4 = *reinterpret_cast<const float4*>(w + (q < 2 ? ca : cb) + (q & 1) * 4);
+        const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = 4 * q + k;
+          const float gr = g[u][i] * r;
+          dw[u][i] = fmaf(gr, x[i], dw[u][i]);
+          x[i] = fmaf(wv[k], gr, -c * x[i]);
+        }
+      }
+      *reinterpret_cast<uint4*>(dr + base + ca) = rope_pack(x);
+      *reinterpret_cast<uint4*>(dr + base + cb) = rope_pack(x + 8);
     }
   }
 
   // dw of the CTA: lanes with the same channels, then the warps in order
-  const int n_dw = per_token ? A.H * A.d : A.d;
-  for (int i = threadIdx.x; i < n_dw; i += blockDim.x) s_dw[i] = 0.f;
+  const int n_dw = per_token ? A.H * A.d : A.d, n_thr = A.tpt * A.groups;
+  for (int i = tid; i < n_dw; i += n_thr) s_dw[i] = 0.f;
   if (!per_token) {
 #pragma unroll
     for (int u = 1; u < U; ++u)
@@ -334,20 +376,20 @@ rope_bwd_kernel(const __grid_constant__ RopeArgs<NF> A) {
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < 16; ++i) dw[u][i] = rope_lane_sum(dw[u][i], same, 32);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+  const int lane = tid & 31, warp = tid >> 5;
+  for (int w = 0; w < n_thr / 32; ++w) {
     __syncthreads();
     if (warp != w || lane >= same) continue;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int id = lane_t + u * A.tpt, base = per_token ? id / A.upd * A.d : 0;
+      const int id = lane_t + u * A.tpt, base = per_token ? (id - o) * 16 : 0;
       if (per_token ? id >= A.units : u > 0) break;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s_dw[base + (i < 8 ? ca + i : cb + i - 8)] += dw[u][i];
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n_dw; i += blockDim.x) A.part[(size_t)blockIdx.x * n_dw + i] = s_dw[i];
+  for (int i = tid; i < n_dw; i += n_thr) A.part[(size_t)blockIdx.x * n_dw + i] = s_dw[i];
 }
 
 // dweight[c] = sum of the CTAs' parts, in a fixed order: 32 channels per CTA, 16 threads a
@@ -357,8 +399,10 @@ rope_dweight_kernel(const float* __restrict__ part, int n_part, int n_dw, float*
   __shared__ float s[16][33];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
   float v = 0.f;
-  if (c < n_dw)
+  if (c < n_dw) {
+#pragma unroll 8
     for (int i = k; i < n_part; i += 16) v += part[(size_t)i * n_dw + c];
+  }
   s[k][threadIdx.x & 31] = v;
   __syncthreads();
   if (k == 0 && c < n_dw) {
