@@ -547,7 +547,7 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBbCount; ++i) {
       const bool rows = i == kBbP || i == kBbP + 1 || i == kBbRd || i == kBbDS || i == kBbDS + 1;
-      mbar_init(&bars[i], rows ? (is_dq ? 4 : 8) : i == kBbDone ? 2 : 1);
+      mbar_init(&bars[i], rows ? 8 : i == kBbDone ? 2 : 1);
     }
     fence_mbar_init();
   }
@@ -707,7 +707,7 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
           ok = ring0(j) && wait(&bars[kBbDS + (j & 1)], (j >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          mma_accumulate<HD>(lead, tmem + L::kAcc0, tmem + (j & 1 ? L::kS1 : L::kS0), 32, slot0(j), j > 0);
+          mma_accumulate<HD>(lead, tmem + L::kAcc0, tmem + (j & 1 ? L::kS1 : L::kS0), 64, slot0(j), j > 0);
           commit_if(lead, &bars[kBbAcc + (j & 1)]);
           commit_if(lead, &e0[j % kRing0]);
         }
@@ -749,73 +749,60 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
         nl = b[0];
         nd = b[64];
       }
-      // valid key columns of each half of tile j for this row (the same for a warp's rows),
-      // v0 | v1 << 8; read one tile ahead
+      // valid key columns of this half of tile j for this row (the same for a warp's rows),
+      // read one tile ahead
       auto columns = [&](int j) {
         if (j >= n_iter) return 0;
-        int v[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (j < d0) {
-            v[u] = max(0, min(64, D.ncur - j * 128 - u * 64));
-          } else {
-            const int e = BLK == 64 ? 2 * (j - d0) + u : j - d0;
-            const uint32_t pe = e < cnt ? entries[e] : 0u;
-            const int len = (pe & bit) ? block_len(D, (pe >> 4) & 0xFFF) : 0;
-            v[u] = BLK == 64 ? len : max(0, min(64, len - u * 64));
-          }
-        }
-        return v[0] | v[1] << 8;
+        if (j < d0) return max(0, min(64, D.ncur - j * 128 - wg * 64));
+        const int e = BLK == 64 ? 2 * (j - d0) + wg : j - d0;
+        const uint32_t pe = e < cnt ? entries[e] : 0u;
+        const int len = (pe & bit) ? block_len(D, (pe >> 4) & 0xFFF) : 0;
+        return BLK == 64 ? len : max(0, min(64, len - wg * 64));
       };
-      const uint32_t s_row = t_row + (wg ? L::kS1 : L::kS0);
-      int v_next = columns(wg);
+      int v_next = columns(0);
 #pragma unroll 1
-      for (int j = wg; ok && j < n_iter; j += 2) {
+      for (int j = 0; ok && j < n_iter; ++j) {
         const int v = v_next;
-        v_next = columns(j + 2);
-        if (!(ok = wait(&bars[kBbS + wg], (j >> 1) & 1))) break;
+        v_next = columns(j + 1);
+        const uint32_t s_col = t_row + (j & 1 ? L::kS1 : L::kS0) + wg * 64;
+        if (!(ok = wait(&bars[kBbS + (j & 1)], (j >> 1) & 1))) break;
         tc_fence_after();
-        // P in fp32 over S, then dS, in loops of 32 columns: code that stays in the
-        // instruction cache is worth more here than values that stay in registers
-#pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          const int nv = (v >> (ch >> 1) * 8 & 255) - (ch & 1) * 32;   // valid columns from here on
-          if (nv <= 0) continue;
-          float s[32];
-          tmem_ld32(s_row + ch * 32, s);
+        float s[64], g[64];
+        if (v > 0) {
+          tmem_ld32(s_col, s);
+          tmem_ld32(s_col + 32, s + 32);
           tmem_ld_wait();
           reg_fence32(s);
+          reg_fence32(s + 32);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = ex2_approx(fmaf(s[i], c, nl));
-          if (nv < 32) {
+          for (int i = 0; i < 64; ++i) s[i] = ex2_approx(fmaf(s[i], c, nl));
+          if (v < 64) {                             // keys past the block's end
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i >= nv) s[i] = 0.f;
+            for (int i = 0; i < 64; ++i)
+              if (i >= v) s[i] = 0.f;
           }
-          tmem_st32(s_row + ch * 32, s);
         }
-        if (!(ok = wait(&bars[kBbDP + wg], (j >> 1) & 1))) break;
+        if (!(ok = wait(&bars[kBbDP + (j & 1)], (j >> 1) & 1))) break;
         tc_fence_after();
-        tmem_st_wait();
-#pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          float s[32], g[32], pk[16];
-          const bool any = (v >> (ch >> 1) * 8 & 255) > (ch & 1) * 32;
-          if (any) {
-            tmem_ld32(s_row + ch * 32, s);
-            tmem_ld32(t_row + L::kDP + ch * 32, g);
-            tmem_ld_wait();
-            reg_fence32(s);
-            reg_fence32(g);
-          }
-          if (ch == 3) warp_arrive(&bars[kBbRd]);
+        if (v > 0) {
+          tmem_ld32(t_row + L::kDP + wg * 64, g);
+          tmem_ld32(t_row + L::kDP + wg * 64 + 32, g + 32);
+          tmem_ld_wait();
+          reg_fence32(g);
+          reg_fence32(g + 32);
+        }
+        warp_arrive(&bars[kBbRd]);
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          float pk[16];
+          const float *p = s + ch * 32, *x = g + ch * 32;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            pk[i] = any ? pack_bf16(s[2 * i] * (g[2 * i] + nd), s[2 * i + 1] * (g[2 * i + 1] + nd)) : 0.f;
-          tmem_st16(s_row + ch * 16, pk);
+            pk[i] = v > 0 ? pack_bf16(p[2 * i] * (x[2 * i] + nd), p[2 * i + 1] * (x[2 * i + 1] + nd)) : 0.f;
+          tmem_st16(s_col + ch * 16, pk);
         }
         tmem_st_wait();
-        warp_arrive(&bars[kBbDS + wg]);
+        warp_arrive(&bars[kBbDS + (j & 1)]);
       }
       if (run) ok = wait(&bars[kBbDone], 0) && ok;
       tc_fence_after();
