@@ -485,23 +485,21 @@ __device__ __forceinline__ void store_box(const void* src, const CUtensorMap* m,
                  ::"l"(m), "r"(smem_u32(src)), "r"(x), "r"(row), "r"(frame) : "memory");
 }
 
-// The stores issued by this thread have read shared memory, and their writes are done.
-__device__ __forceinline__ void stores_done() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+// The stores issued by this thread have read shared memory (their writes end with the kernel).
+__device__ __forceinline__ void stores_read() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// Whole-warp wait for an mbarrier's phase, until the deadline (in clocks) at the latest.
-// Small, because the loops of all roles together have to stay within the 32 KB of the
-// instruction cache.
+// Whole-warp wait for an mbarrier's phase, until the deadline (in clocks) at the latest.  It
+// branches on votes alone, so the warp leaves it together (what follows runs in uniform
+// registers).  Small, because the loops of all roles together have to stay within the 32 KB of
+// the instruction cache.
 __device__ __forceinline__ bool wait_until(uint64_t* bar, uint32_t parity, long long deadline) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 t;\n\t"
-      "W%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D%=;\n\t"
-      "mov.u64 t, %%clock64;\n\tsetp.lt.s64 q, t, %3;\n\t@q bra W%=;\n\t"
-      "D%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "l"(deadline) : "memory");
-  return __all_sync(0xffffffffu, ok) != 0;
+#pragma unroll 1
+  for (;;) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, clock64() >= deadline)) return false;
+  }
 }
 
 template <int HD, int BLK, bool is_dq>
@@ -817,7 +815,7 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
         const int q2 = BLK == 64 && r ? qbB : qbA, row = (q2 % D.nbpf) * BLK + (BLK == 128 ? r * 64 : 0);
         if (q2 >= 0 && row < D.T)
           store_box(in0 + wg * L::kRegion + r * 64 * 128, &P.dq3, h * HD + wg * 64, row, q2 / D.nbpf);
-        stores_done();
+        stores_read();
       }
     } else {
       const uint32_t bit = r < 64 ? 1u : 2u;
@@ -914,7 +912,7 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
         if (row < (kt.kind == 0 ? D.ncur : D.T))
           for (int c = 0; c < L::NH; ++c)
             store_box(out + c * L::kRegion + r * 64 * 128, m, h * HD + c * 64, row, f);
-        stores_done();
+        stores_read();
       }
     }
     tc_fence_before();
