@@ -561,6 +561,11 @@ int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
     p.kh = p.kc3;
     p.vh = p.vc3;
   }
+  p.dq = static_cast<__nv_bfloat16*>(b.dq);
+  p.dk_cur = static_cast<__nv_bfloat16*>(b.dk_cur);
+  p.dv_cur = static_cast<__nv_bfloat16*>(b.dv_cur);
+  p.dk_cache = static_cast<__nv_bfloat16*>(b.dk_cache);
+  p.dv_cache = static_cast<__nv_bfloat16*>(b.dv_cache);
   // outputs: 3-D per frame where query blocks or lists address them, 2-D for the dense chunk
   if ((rc = encode_rows(&p.dq3, b.dq, HD, D.T, D.Fc)) != LF_OK) return rc;
   if ((rc = encode_rows(D.kc > 0 ? &p.dk3 : &p.dk2, b.dk_cur, HD, D.kc > 0 ? D.T : D.ncur,

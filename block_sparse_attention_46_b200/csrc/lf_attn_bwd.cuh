@@ -266,8 +266,9 @@ bwd_transpose_kernel(const uint32_t* __restrict__ plan, const int32_t* __restric
 // waits for that one's completion.
 // ---------------------------------------------------------------------------------
 constexpr int kBwdThreads = 384;
-// Register split, as in the forward kernel: 128 x 72 + 256 x 216 = 384 x 168.
-constexpr int kBwdLaunchRegs = 168, kBwdLowRegs = 72, kBwdHighRegs = 216;
+// Register split: 128 x 136 + 256 x 184 = 384 x 168 (the issuers need more than the forward kernel's
+// 72, with which they spill inside their loops: 3257 us for the large chunk against 3160).
+constexpr int kBwdLaunchRegs = 168, kBwdLowRegs = 136, kBwdHighRegs = 184;
 static_assert(128 * kBwdLowRegs + 256 * kBwdHighRegs <= kBwdThreads * kBwdLaunchRegs, "register split");
 
 struct BwdParams {
@@ -275,6 +276,7 @@ struct BwdParams {
   // 3-D per frame, boxes of 64 x 64
   CUtensorMap q2, q3, g2, g3, kc2, kc3, vc2, vc3, kh, vh;
   CUtensorMap dq3, dk2, dk3, dkh, dv2, dv3, dvh;   // outputs, boxes of 64 x 64
+  __nv_bfloat16 *dq, *dk_cur, *dv_cur, *dk_cache, *dv_cache;
   const uint32_t* plan;
   const int32_t* plan_cnt;
   BwdRows rows;
@@ -446,21 +448,16 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// N (64 or 128) accumulators of a row, times f, as bf16 (zeros when !any) into the row of a
-// tile in shared memory, in the 128-byte swizzle of the tensor maps.
+// N (64 or 128) accumulators of a row, times f, as bf16 into the row of a tile in shared memory,
+// in the 128-byte swizzle of the tensor maps.
 template <int N>
-__device__ __forceinline__ void stage_row(uint8_t* tile, int r, uint32_t taddr, float f, bool any) {
+__device__ __forceinline__ void stage_row(uint8_t* tile, int r, uint32_t taddr, float f) {
 #pragma unroll 1
   for (int ch = 0; ch < N / 32; ++ch) {
     float v[32];
-    if (any) {
-      tmem_ld32(taddr + ch * 32, v);
-      tmem_ld_wait();
-      reg_fence32(v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.f;
-    }
+    tmem_ld32(taddr + ch * 32, v);
+    tmem_ld_wait();
+    reg_fence32(v);
     uint8_t* row = tile + (ch >> 1) * (128 * 128) + r * 128;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -542,6 +539,26 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
     }
   }
 
+  // nothing to stream (a key tile that no query attends to): zeros, without the machinery
+  if (n_iter == 0) {
+    for (int i = threadIdx.x; i < 128 * (HD / 8); i += kBwdThreads) {
+      const int r = i / (HD / 8), col = h * HD + i % (HD / 8) * 8;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      if (is_dq) {
+        const int qb = BLK == 64 && r >= 64 ? qbB : qbA, i0 = BLK == 64 ? r & 63 : r;
+        if (qb < 0 || i0 >= block_len(D, qb % D.nbpf)) continue;
+        const size_t tok = (size_t)(qb / D.nbpf) * D.T + (qb % D.nbpf) * BLK + i0;
+        *reinterpret_cast<uint4*>(P.dq + tok * D.H * HD + col) = zero;
+      } else if (kt.row + r < D.T) {                // only tiles with lists can be empty
+        const bool cur = kt.kind == 2;
+        const size_t at = ((size_t)(cur ? kt.frame : P.slots[D.S + kt.frame]) * D.T + kt.row + r) * D.H * HD + col;
+        *reinterpret_cast<uint4*>((cur ? P.dk_cur : P.dk_cache) + at) = zero;
+        *reinterpret_cast<uint4*>((cur ? P.dv_cur : P.dv_cache) + at) = zero;
+      }
+    }
+    return;
+  }
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBbCount; ++i) {
       const bool rows = i == kBbP || i == kBbP + 1 || i == kBbRd || i == kBbDS || i == kBbDS + 1;
@@ -560,8 +577,8 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
   uint8_t* in0 = smem + L::kIn0;
   uint8_t* in1 = smem + L::kIn1;
   // the window of dynamic shared memory starts on 1024 bytes (swizzled tiles need it)
-  const bool run = n_iter > 0 && (smem_u32(smem) & 1023u) == 0;
-  if (n_iter > 0 && !run && threadIdx.x == 0) record_status(LF_ERR_CUDA);
+  const bool run = (smem_u32(smem) & 1023u) == 0;
+  if (!run && threadIdx.x == 0) record_status(LF_ERR_CUDA);
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_until(bar, parity, deadline); };
   // for what has been issued and has to end before the CTA may exit: a limit of its own
   auto drain = [&](uint64_t* bar, uint32_t parity) {
@@ -806,12 +823,12 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
       tc_fence_after();
       // 64 channels each (d = 64: the first warpgroup alone), over Q, which no MMA reads any more
       const bool mine = HD == 128 || wg == 0;
-      if (mine && (ok || n_iter == 0)) {
-        stage_row<64>(in0 + wg * L::kRegion, r, t_row + L::kAcc0 + wg * 64, D.scale, n_iter > 0);
+      if (mine && ok) {
+        stage_row<64>(in0 + wg * L::kRegion, r, t_row + L::kAcc0 + wg * 64, D.scale);
         fence_proxy_async_smem();
       }
       named_bar_sync(kNbStore + wg, 128);
-      if (mine && (ok || n_iter == 0) && r < 2) {   // a box each
+      if (mine && ok && r < 2) {   // a box each
         const int q2 = BLK == 64 && r ? qbB : qbA, row = (q2 % D.nbpf) * BLK + (BLK == 128 ? r * 64 : 0);
         if (q2 >= 0 && row < D.T)
           store_box(in0 + wg * L::kRegion + r * 64 * 128, &P.dq3, h * HD + wg * 64, row, q2 / D.nbpf);
@@ -898,12 +915,12 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
       tc_fence_after();
       // dk over K and dv over V, which no MMA reads any more
       uint8_t* out = wg == 0 ? in0 : in1;
-      if (ok || n_iter == 0) {
-        stage_row<HD>(out, r, t_row + (wg == 0 ? L::kAcc0 : L::kAcc1), wg == 0 ? D.scale : 1.f, n_iter > 0);
+      if (ok) {
+        stage_row<HD>(out, r, t_row + (wg == 0 ? L::kAcc0 : L::kAcc1), wg == 0 ? D.scale : 1.f);
         fence_proxy_async_smem();
       }
       named_bar_sync(kNbStore + wg, 128);
-      if ((ok || n_iter == 0) && r < 2) {           // a box each
+      if (ok && r < 2) {                            // a box each
         const int row = kt.row + r * 64;
         const int f = kt.kind == 0 ? -1 : kt.kind == 2 ? kt.frame
                                         : P.slots[kt.kind == 1 ? kt.frame : D.S + kt.frame];
