@@ -533,7 +533,7 @@ int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
   const lf::KeyTiles K = lf::key_tiles(D, cache_grad);
   const int plan_ctas = lf::cdiv(lf::tile_count(D), lf::kPlanWarps);
   const int padded = D.nqb * D.B + lf::bwd_dense_boxes(D) * 64 - D.ncur;
-  const int row_ctas = lf::cdiv(padded, lf::kPrepThreads / (D.d / 8));
+  const int row_ctas = lf::cdiv(padded, lf::kPrepRows * (lf::kPrepThreads / (D.d / 8)));
   const int longest = D.nsel > D.kc ? D.nsel : D.kc;
   lf::bwd_prep_kernel<<<dim3(plan_ctas + row_ctas, D.H), lf::kPrepThreads,
                         lf::kPlanWarps * 2 * longest * sizeof(int32_t), st>>>(

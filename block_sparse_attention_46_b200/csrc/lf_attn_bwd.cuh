@@ -35,7 +35,7 @@ __host__ __device__ inline int bwd_blk_boxes(const Dims& D) { return D.nqb * (D.
 // chunk came on top of the rows' 13): per head (grid.y) the first plan_ctas CTAs make key plans,
 // a warp each, the others the row values with d / 8 threads per row and 16-byte loads.  Also
 // zeroes the entry counter of the transposed plans.
-constexpr int kPrepThreads = kPlanWarps * 32;
+constexpr int kPrepThreads = kPlanWarps * 32, kPrepRows = 4;   // rows per thread, loaded at once
 
 __global__ void __launch_bounds__(kPrepThreads)
 bwd_prep_kernel(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ dout,
@@ -58,44 +58,56 @@ bwd_prep_kernel(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __re
     return;
   }
   const int lg = D.d == 128 ? 4 : 3, per = 1 << lg;      // threads per row
-  const int p = ((blockIdx.x - plan_ctas) * kPrepThreads + threadIdx.x) >> lg;
-  const int part = threadIdx.x & (per - 1), h = blockIdx.y;
+  const int part = threadIdx.x & (per - 1), h = blockIdx.y, step = kPrepThreads >> lg;
   const int blk_rows = D.nqb * D.B, dense_rows = bwd_dense_boxes(D) * 64;
-  // p: padded row; then the dense padding
-  int tok = -1;
-  if (p < blk_rows) {
-    const int qb = p / D.B, i = p % D.B;
-    if (i < block_len(D, qb % D.nbpf)) tok = (qb / D.nbpf) * D.T + (qb % D.nbpf) * D.B + i;
+  // p0 + k step: padded rows; then the dense padding
+  const int p0 = (blockIdx.x - plan_ctas) * (kPrepRows * step) + (threadIdx.x >> lg);
+  int tok[kPrepRows];
+  uint4 a[kPrepRows], b[kPrepRows];
+#pragma unroll
+  for (int k = 0; k < kPrepRows; ++k) {
+    const int p = p0 + k * step;
+    tok[k] = -1;
+    a[k] = b[k] = make_uint4(0, 0, 0, 0);
+    if (p < blk_rows) {
+      const int qb = D.B == 128 ? p >> 7 : p >> 6, f = qb / D.nbpf;
+      const int t = p - f * D.nbpf * D.B;              // in the padded frame
+      if (t < D.T) tok[k] = f * D.T + t;
+    }
+    if (tok[k] >= 0) {
+      const size_t off = ((size_t)tok[k] * D.H + h) * D.d + part * 8;
+      a[k] = *reinterpret_cast<const uint4*>(out + off);
+      b[k] = *reinterpret_cast<const uint4*>(dout + off);
+    }
   }
-  float s = 0.f;
-  if (tok >= 0) {
-    const size_t off = ((size_t)tok * D.H + h) * D.d + part * 8;
-    const uint4 a = *reinterpret_cast<const uint4*>(out + off);
-    const uint4 b = *reinterpret_cast<const uint4*>(dout + off);
-    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int k = 0; k < kPrepRows; ++k) {
+    const int p = p0 + k * step;
+    const uint32_t wa[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, wb[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       s = fmaf(__uint_as_float(wa[i] << 16), __uint_as_float(wb[i] << 16), s);
       s = fmaf(__uint_as_float(wa[i] & 0xffff0000u), __uint_as_float(wb[i] & 0xffff0000u), s);
     }
-  }
-  for (int o = 1; o < per; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (part != 0) return;
-  float nl = -INFINITY;
-  if (tok >= 0) {
-    const float l = lse[(size_t)h * D.ncur + tok];
-    if (l != -INFINITY) nl = -l * 1.4426950408889634f;
-  }
-  auto put = [&](float* base, size_t box0, int row) {
-    float* b = base + (box0 + row / 64) * kBoxFloats + row % 64;
-    b[0] = nl;
-    b[64] = -s;
-  };
-  if (p < blk_rows) {
-    if (blk) put(R.blk, (size_t)h * bwd_blk_boxes(D), p);
-    if (tok >= 0) put(R.dense, (size_t)h * bwd_dense_boxes(D), tok);
-  } else if (p - blk_rows < dense_rows - D.ncur) {
-    put(R.dense, (size_t)h * bwd_dense_boxes(D), D.ncur + p - blk_rows);
+    for (int o = 1; o < per; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (part != 0) continue;
+    float nl = -INFINITY;
+    if (tok[k] >= 0) {
+      const float l = lse[(size_t)h * D.ncur + tok[k]];
+      if (l != -INFINITY) nl = -l * 1.4426950408889634f;
+    }
+    auto put = [&](float* base, size_t box0, int row) {
+      float* x = base + (box0 + row / 64) * kBoxFloats + row % 64;
+      x[0] = nl;
+      x[64] = -s;
+    };
+    if (p < blk_rows) {
+      if (blk) put(R.blk, (size_t)h * bwd_blk_boxes(D), p);
+      if (tok[k] >= 0) put(R.dense, (size_t)h * bwd_dense_boxes(D), tok[k]);
+    } else if (p - blk_rows < dense_rows - D.ncur) {
+      put(R.dense, (size_t)h * bwd_dense_boxes(D), D.ncur + p - blk_rows);
+    }
   }
 }
 
