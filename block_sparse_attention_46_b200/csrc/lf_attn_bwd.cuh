@@ -261,16 +261,26 @@ bwd_transpose_kernel(const uint32_t* __restrict__ plan, const int32_t* __restric
 //            dP^T = V dout^T, dS^T as bf16 beside P^T, dk += dS^T Q
 //
 // Four warps issue (two TMA, two tcgen05.mma: scores and dP by one, the accumulating products
-// by the other, so that neither waits behind the other's operands), eight make P and dS.
-// Tensor memory has 512 columns; the accumulators take 128 (dq) or 256 (dk and dv).
-//
-//   dq: buffers S0, S1 and one of dP.  Warpgroup w takes tiles w, w + 2, ... whole, a thread
-//   one row of 128 columns: while one warpgroup is at the exponentials of its tile (1024 clk
-//   of the special-function units), the other multiplies and stores dS of its own.
+// by the other, so that neither waits behind the other's operands), two warpgroups make P and
+// dS, a thread one row of columns [64 w, 64 w + 64) of every tile.  Tensor memory has 512
+// columns; the accumulators take 128 (dq) or 256 (dk and dv):
+//   dq: buffers S0, S1 and one of dP.  S of tile j + 1 and, once this tile's is read, dP of
+//   tile j + 1 run under the exponentials of tile j.
 //   dk, dv: buffers X0, X1.  Tile j has S in X[j & 1] and dP in the other one, P and dS both
 //   go over S, so dP's buffer is free for the next tile's S once it has been read, and the
-//   exponentials of tile j + 1 overlap dk of tile j and dP of tile j + 1.  Warpgroup w takes
-//   columns [64 w, 64 w + 64) of every tile.
+//   exponentials of tile j + 1 overlap dk of tile j and dP of tile j + 1.
+//
+// What bounds it: the tensor pipe is active 62 % of the cycles (480p chunk with cache
+// gradients: 1.00 ms, 467 MB read, 177 MB written).  A 128 x 128 tile takes 2180 clk for dq (three
+// products of 512) and 2900 for dk and dv (four), the difference being the chain through one
+// tile: S, exponentials (1024 clk of the special-function units), dP, dS, the product that
+// frees the buffer for the next S, and an mbarrier's 150-250 clk at each hand-off.  Measured
+// instead, on the 480p chunk: dq's warpgroups on alternate tiles 8 % slower; left operands in
+// tensor memory and units of 64 columns (products at the full rate beside the copies, but
+// twice the hand-offs) 10 %, also with two teams of eight row warps; a quarter or a third of
+// the exponentials on the multiply-add units 1 %; own tiles loaded before the allocation of
+// tensor memory 2 %.  More code in the loops costs by itself: all roles' loops share an
+// instruction cache of 32 KB.
 //
 // A barrier that is waited for every other tile, or whose next completion does not depend on
 // the waiting thread, exists twice, one for even and one for odd tiles: a wait on a parity
@@ -337,7 +347,7 @@ static_assert(BwdLayout<128>::kIn0 % 1024 == 0 && BwdLayout<128>::kBytes <= 227 
 
 // Tensor-core and copy instructions of one elected lane, issued from code that the whole warp
 // runs: their operands (descriptors, addresses) then stay in uniform registers.  Issued from
-// a lane-0 branch, 8 MMAs took the issuer 850-1100 clk instead of the 560 that they run.
+// a lane-0 branch, 8 MMAs took the issuer 850-1100 clk; this way 170-230, less than they run.
 __device__ __forceinline__ uint32_t elect_lane() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"

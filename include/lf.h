@@ -224,6 +224,8 @@ int lf_block_sparse_attn(const lf_shape* shape, const void* q, const void* k_cur
  * meet in one place).  Outputs must not overlap inputs or each other.  A row that attends to
  * nothing (lse = -inf) gets dq = 0 and gives nothing to dk and dv.  Products run on bf16
  * tensor cores with P and dS rounded to bf16, sums in fp32; each gradient is rounded once.
+ * As in the forward pass, query blocks and key blocks share 128-row tiles: an infinity or NaN
+ * in a block may also reach the gradients of the block that shares its tile.
  * workspace: at least lf_attn_backward_workspace_size(shape) bytes, 256-byte aligned, for
  * this call alone until it has finished on the GPU.  LF_ERR_BAD_INDEX and LF_ERR_TIMEOUT as
  * for lf_block_sparse_attn. */
