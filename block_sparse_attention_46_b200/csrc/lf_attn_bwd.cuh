@@ -271,16 +271,19 @@ bwd_transpose_kernel(const uint32_t* __restrict__ plan, const int32_t* __restric
 //   exponentials of tile j + 1 overlap dk of tile j and dP of tile j + 1.
 //
 // What bounds it: the tensor pipe is active 62 % of the cycles (480p chunk with cache
-// gradients: 1.00 ms, 467 MB read, 177 MB written).  A 128 x 128 tile takes 2180 clk for dq (three
-// products of 512) and 2900 for dk and dv (four), the difference being the chain through one
-// tile: S, exponentials (1024 clk of the special-function units), dP, dS, the product that
-// frees the buffer for the next S, and an mbarrier's 150-250 clk at each hand-off.  Measured
+// gradients: 1.00 ms at 1.69 GHz, 467 MB read, 177 MB written).  A 128 x 128 tile takes 2160-2200
+// clk for dq (1536 of products) and 2890-2940 for dk and dv (2048).  The rest is taken to be
+// the chain through one tile: S, exponentials (1024 clk of the special-function units), dP,
+// dS, the product that frees the buffer for the next S, with 130-150 clk per mbarrier hop.
+// A CTA's start and end add 7300-9500 clk, which the short key tiles feel most.  Measured
 // instead, on the 480p chunk: dq's warpgroups on alternate tiles 8 % slower; left operands in
-// tensor memory and units of 64 columns (products at the full rate beside the copies, but
-// twice the hand-offs) 10 %, also with two teams of eight row warps; a quarter or a third of
-// the exponentials on the multiply-add units 1 %; own tiles loaded before the allocation of
-// tensor memory 2 %.  More code in the loops costs by itself: all roles' loops share an
-// instruction cache of 32 KB.
+// tensor memory and units of 64 columns 7-15 %, with two teams of eight row warps 10 %; part
+// of the exponentials on the multiply-add units 1 %; own tiles loaded before the allocation
+// of tensor memory 2-3 %; no register split 3 %.
+//
+// P and dS enter their products rounded to bf16, as tensor-core operands have to be: each
+// product's term is off by 2^-8 relative at most.  Outputs' relative error is then 0.0024 to
+// 0.0025 against 64 bits; fp32 operands and one rounding at the end give 0.0017.
 //
 // A barrier that is waited for every other tile, or whose next completion does not depend on
 // the waiting thread, exists twice, one for even and one for odd tiles: a wait on a parity
@@ -288,8 +291,8 @@ bwd_transpose_kernel(const uint32_t* __restrict__ plan, const int32_t* __restric
 // waits for that one's completion.
 // ---------------------------------------------------------------------------------
 constexpr int kBwdThreads = 384;
-// Register split: 128 x 136 + 256 x 184 = 384 x 168 (the issuers need more than the forward kernel's
-// 72, with which they spill inside their loops: 3257 us for the large chunk against 3160).
+// Register split: 128 x 136 + 256 x 184 = 384 x 168.  Issuers at 120, 136 and 152: single calls
+// of the large chunk 3231, 3161 and 3184 us, the other sizes alike within 2 %.
 constexpr int kBwdLaunchRegs = 168, kBwdLowRegs = 136, kBwdHighRegs = 184;
 static_assert(128 * kBwdLowRegs + 256 * kBwdHighRegs <= kBwdThreads * kBwdLaunchRegs, "register split");
 
@@ -347,7 +350,7 @@ static_assert(BwdLayout<128>::kIn0 % 1024 == 0 && BwdLayout<128>::kBytes <= 227 
 
 // Tensor-core and copy instructions of one elected lane, issued from code that the whole warp
 // runs: their operands (descriptors, addresses) then stay in uniform registers.  Issued from
-// a lane-0 branch, 8 MMAs took the issuer 850-1100 clk; this way 170-230, less than they run.
+// a lane-0 branch, 8 MMAs took the issuer 850-1100 clk instead of the 560 that they run.
 __device__ __forceinline__ uint32_t elect_lane() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"

@@ -224,11 +224,11 @@ int lf_block_sparse_attn(const lf_shape* shape, const void* q, const void* k_cur
  * meet in one place).  Outputs must not overlap inputs or each other.  A row that attends to
  * nothing (lse = -inf) gets dq = 0 and gives nothing to dk and dv.  Products run on bf16
  * tensor cores with P and dS rounded to bf16, sums in fp32; each gradient is rounded once.
- * As in the forward pass, query blocks and key blocks share 128-row tiles: an infinity or NaN
- * in a block may also reach the gradients of the block that shares its tile.
+ * As in the forward pass, tiles are 128 rows: an infinity or NaN in a row may also reach the
+ * gradients of rows that attend to its tile, or share it, without attending to that row.
  * workspace: at least lf_attn_backward_workspace_size(shape) bytes, 256-byte aligned, for
  * this call alone until it has finished on the GPU.  LF_ERR_BAD_INDEX and LF_ERR_TIMEOUT as
- * for lf_block_sparse_attn. */
+ * for lf_block_sparse_attn, but the waits' limit (2 s) counts from the start of each CTA. */
 size_t lf_attn_backward_workspace_size(const lf_shape* shape);
 int lf_block_sparse_attn_backward(const lf_shape* shape, const void* q, const void* k_cur,
                                   const void* v_cur, const void* k_cache, const void* v_cache,
