@@ -509,16 +509,18 @@ def _rope_tokens(H, d, T, t, name, device, contiguous):
     strides = t.stride()
     if (strides[-1] != 1 and d > 1) or (strides[-2] != d and H > 1):
         raise ValueError(f"{what}: a token's H * d channels of {name} must be contiguous")
-    stride = step = 0
+    stride = step = None                              # None: only dimensions of one token yet
     for s, st in zip(shape[-3::-1], strides[-3::-1]):
         if s == 1:
             continue
-        if step == 0:
+        if step is None:
+            if st < row:                              # broadcast or overlapping tokens
+                raise ValueError(f"{what}: {name}'s tokens share memory")
             stride = step = st
         if st != step:
             raise ValueError(f"{what}: {name}'s tokens are not at one stride")
         step *= s
-    return t.data_ptr(), stride or row, n
+    return t.data_ptr(), row if stride is None else stride, n
 
 
 def _frames(n_frames, v, name):

@@ -69,3 +69,30 @@ def test_rope_validation(lib):
     twice, _k = _i32([1, 2, 1])
     assert bwd(x=None) == 1 and bwd(w=None) == 1 and bwd(dw=None) == 1 and bwd(dxs=64) == 1
     assert bwd(ins=twice) == 1 and bwd(ws=size - 1) == 5
+
+
+def test_rope_tokens_stay_in_their_storage():
+    """Token strides that the kernels cannot follow are refused: broadcast tokens (stride 0, also
+    under an outer dimension that has a stride) and tokens that overlap.  CPU tensors only."""
+    import torch
+    H, d, T, F = 2, 64, 6, 3
+
+    def zeros(*size):
+        return torch.zeros(*size, dtype=torch.bfloat16)
+
+    def look(x):
+        return lf._rope_tokens(H, d, T, x, "x", torch.device("cpu"), False)
+
+    for x in (zeros(F, 1, H, d).expand(F, T, H, d), zeros(1, 1, H, d).expand(F, T, H, d),
+              zeros(1, T, H, d).expand(F, T, H, d), zeros(1, H, d).expand(F * T, H, d),
+              zeros(4000).as_strided((F, T, H, d), (T * 64, 64, 64, 1))):
+        with pytest.raises(ValueError):
+            look(x)
+    for x, stride in ((zeros(F, T, H, d), H * d), (zeros(F * T, H, d), H * d),
+                      (zeros(F, T, 3 * H, d)[:, :, H:2 * H], 3 * H * d),
+                      (zeros(F, T, 3, H, d)[:, :, 1], 3 * H * d),
+                      (zeros(F * T, 2 * H, d)[:, :H], 2 * H * d)):
+        address, step, n = look(x)
+        assert (step, n) == (stride, F)
+        last = x.storage_offset() + (n * T - 1) * step + H * d
+        assert last <= x.untyped_storage().nbytes() // 2
