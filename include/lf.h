@@ -273,7 +273,9 @@ typedef struct lf_rope {
  * in_slots, out_slots, frame_pos: HOST arrays of n_frames, read during the call only.
  * weight: fp32, 16-byte aligned, for norm != LF_NORM_NONE; NULL without a norm.
  * out may be x when strides and slots agree frame by frame; otherwise they must not overlap.
- * Without pairs and norm the call moves frames into cache slots (values). */
+ * Without pairs and norm the call moves frames into cache slots (values).
+ * With a norm, the squares are summed in fp32: a row's root mean square has to be below 2^57,
+ * and above 2^-57 where eps is so small that it does not cover the mean square. */
 int lf_rope_frames(const lf_rope* rope, const void* x, int64_t x_stride, int32_t n_in,
                    const int32_t* in_slots, const int32_t* frame_pos, const float* weight,
                    void* out, int32_t n_out, const int32_t* out_slots, cudaStream_t stream);

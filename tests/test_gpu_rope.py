@@ -233,3 +233,17 @@ def test_refusals(gpu_lib):
         forward(bad(outs=[0, 1, 1]))
     with pytest.raises(lf.LfError):
         backward(c, workspace=torch.empty(256, dtype=torch.uint8, device="cuda")[:128])
+
+
+@pytest.mark.parametrize("norm", ["head", "row"])
+@pytest.mark.parametrize("power", [-57, -50, -43, 43, 50, 57])
+def test_gradient_of_very_small_and_large_rows(gpu_lib, norm, power):
+    """Rows of root mean square near 2^power, with a gradient along the normed row, so that the
+    projection dx = r (w g - xn mean(w g xn)) takes away about as much as it leaves.  Every term
+    is a product of r and values of the size of g, so fp32 keeps its relative error; the
+    tolerances are those of ordinary rows.  Small rows have eps = 0."""
+    c = case(3, 128, 1, 3, 5, norm=norm, eps=0.0 if power < 0 else 1e-6, seed=power + 100,
+             strided=True)
+    c["x"].mul_(2.0 ** power)                              # exact
+    c["dout"] = (check_forward(c).float() + 0.5 * c["dout"].float()).to(torch.bfloat16)
+    check_backward(c, wide=True)
