@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 from typing import Optional, Sequence
 
@@ -158,7 +159,12 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _slots(v: Sequence[int]):
-    arr = (ctypes.c_int32 * max(len(v), 1))(*[int(x) for x in v])
+    """Host list of int32 for a call.  ctypes would wrap what does not fit and int() cut off a
+    fraction, both silently."""
+    n = [int(x) for x in v]
+    if n and not (-2 ** 31 <= min(n) and max(n) < 2 ** 31 and all(map(operator.eq, n, v))):
+        raise ValueError(f"slots and positions are 32-bit integers, not {list(v)}")
+    arr = (ctypes.c_int32 * max(len(n), 1))(*n)
     return ctypes.cast(arr, _I32P), arr          # keep `arr` alive during the call
 
 
@@ -488,8 +494,10 @@ def make_rope(H, d, n_frames, height, width, pairs, halves=False, norm=None, bas
     (time, height, width), pairing, norm (None, "head" or "row", over the whole token)."""
     if norm not in _NORMS:
         raise ValueError(f"norm must be one of {list(_NORMS)}")
-    return LfRope(H, d, n_frames, height, width, *[int(p) for p in pairs], 1 if halves else 0,
-                  _NORMS[norm], eps, base)
+    sizes = [H, d, n_frames, height, width, *[int(p) for p in pairs]]
+    if not (-2 ** 31 <= min(sizes) and max(sizes) < 2 ** 31):
+        raise ValueError(f"sizes are 32-bit integers, not {sizes}")
+    return LfRope(*sizes, 1 if halves else 0, _NORMS[norm], eps, base)
 
 
 def _rope_tokens(H, d, T, t, name, device, contiguous):

@@ -96,3 +96,29 @@ def test_rope_tokens_stay_in_their_storage():
         assert (step, n) == (stride, F)
         last = x.storage_offset() + (n * T - 1) * step + H * d
         assert last <= x.untyped_storage().nbytes() // 2
+
+
+@pytest.mark.parametrize("far", [2 ** 31, -2 ** 31 - 1, 2 ** 32, 2 ** 63, 0.5])
+def test_integers_are_not_wrapped(lib, far):
+    """Positions and slots that are no 32-bit integers, and sizes that would wrap into valid ones
+    (2^32 + 2 heads), are refused by the binding: the C side sees the wrapped value only."""
+    for name in ("frame_pos", "in_slots", "out_slots"):
+        with pytest.raises(ValueError, match="32-bit"):
+            lf._frames(2, [0, far], name)
+    with pytest.raises(ValueError, match="32-bit"):
+        lf.lf_pool_frames(_shape(), None, [far], None)
+    if far == int(far):
+        with pytest.raises(ValueError, match="32-bit"):
+            lf.make_rope(far + 2 if far > 0 else far, 64, 1, 1, 1, (0, 0, 0))
+        with pytest.raises(ValueError, match="32-bit"):
+            lf.make_rope(2, 64, 1, 1, 1, (far, 0, 0))
+
+
+def test_32_bit_lists_pass_unchanged():
+    import numpy as np
+    import torch
+    ends = [-2 ** 31, -1, 0, 2 ** 31 - 1]
+    for v in (ends, tuple(ends), np.array(ends), torch.tensor(ends), [float(x) for x in ends]):
+        pointer, keep = lf._slots(v)
+        assert list(keep) == ends and pointer[3] == ends[3]
+    assert len(lf._slots([])[1]) == 1
