@@ -538,7 +538,7 @@ int launch_attn_bwd(const Dims& D, const BwdPtrs& b, const int32_t* hist_slots,
   lf::bwd_prep_kernel<<<dim3(plan_ctas + row_ctas, D.H), lf::kPrepThreads,
                         lf::kPlanWarps * 2 * longest * sizeof(int32_t), st>>>(
       static_cast<const __nv_bfloat16*>(b.out), static_cast<const __nv_bfloat16*>(b.dout), b.lse, rows,
-      lf::key_tiles(D, true).n_list() > 0, D.F > 0 ? block_idx : nullptr, D.kc > 0 ? cur_idx : nullptr,
+      K.n_list() > 0, D.F > 0 ? block_idx : nullptr, D.kc > 0 ? cur_idx : nullptr,
       w.attn.plan, w.attn.plan_cnt, w.inv_total, plan_ctas, longest, D);
   if (K.n_list() > 0)
     lf::bwd_transpose_kernel<<<lf::cdiv(K.n_list() * D.H, lf::kInvWarps), lf::kInvWarps * 32, 0, st>>>(

@@ -339,3 +339,21 @@ def test_stalled_wait_times_out_and_context_recovers(gpu_lib):
         lf.lf_debug_configure()
     assert lf.lf_device_status(True) == 4                 # LF_ERR_TIMEOUT
     run_case(ci)
+
+
+def test_detached_dense_chunk_makes_no_block_boxes(gpu_lib):
+    """Without lists of query blocks (a dense chunk, no gradient into the cache) the preparation
+    writes the rows in token order only: 512 bytes per 64 of them, beside the key plans."""
+    ci = small(17, T=300, H=4)
+    t = G.to_dev(ci)
+    bidx, _ = lists(ci.shape, 0)
+    out, lse = forward(ci, t, bidx, None)
+    ws = torch.full((lf.lf_attn_backward_workspace_size(ci.shape),), 255, dtype=torch.uint8,
+                    device="cuda")
+    backward(ci, t, bidx, None, out, dout_for(ci), lse, cache=False, workspace=ws)
+    sh = ci.shape
+    nb, nqb, kf, kb = lf.derived(sh)
+    tiles = -(-nqb // 2)
+    plans = 4 * sh.H * tiles * (1 + sh.n_sink * nb + 2 * kf * kb) + 4
+    dense = sh.H * 2 * -(-sh.n_cur_frames * sh.T // 128) * 512
+    assert int((ws != 255).sum()) <= plans + dense
