@@ -190,11 +190,11 @@ def lf_device_status(reset: bool = True) -> int:
     return load().lf_device_status(1 if reset else 0)
 
 
-def lf_debug_configure(wait_limit_ns: int = 0, stall: bool = False, tail_split: bool = True):
-    """Test hook: wait limit of the device waits, a stalled first CTA, and whether the last
-    partial wave of query tiles may be split (defaults restored by calling it with none)."""
-    _check(load().lf_debug_configure(int(wait_limit_ns), 1 if stall else 0,
-                                     1 if tail_split else 0), "lf_debug_configure")
+def lf_debug_configure(wait_limit_ns: int = 0, stall: int = 0, tail_split: bool = True):
+    """Test hook: wait limit of the device waits, a stalled CTA (True: the first one), and whether
+    the last partial wave of query tiles may be split (defaults restored by calling it with none)."""
+    _check(load().lf_debug_configure(int(wait_limit_ns), int(stall), 1 if tail_split else 0),
+           "lf_debug_configure")
 
 
 def lf_compress(shape, q, k_cache, hist_slots, q_blk, k_blk, k_frm, stream=None):

@@ -1297,7 +1297,7 @@ int lf_select_chunk_cached(const lf_shape* shape, const void* q, const float* k_
 int lf_debug_configure(uint64_t wait_limit_ns, int stall, int tail_split) {
   if (wait_limit_ns > 10ull * lf::kWaitLimitNs) return LF_ERR_INVALID_ARG;
   g_dbg_wait_limit_ns = wait_limit_ns == 0 ? lf::kWaitLimitNs : wait_limit_ns;
-  g_dbg_stall = stall != 0;
+  g_dbg_stall = stall < 0 ? 1 : stall;
   g_dbg_tail_split = tail_split != 0;
   return LF_OK;
 }

@@ -310,7 +310,7 @@ struct BwdParams {
   const int32_t *inv_off, *inv_cnt;
   int n_dq;                   // query tiles of all heads
   long long wait_limit_clk;   // limit of a CTA's waits, from its start
-  int debug_stall;            // test hook, as in the forward kernel
+  int debug_stall;            // test hook: the CTA whose own tiles never come, + 1; 0: none
   int slots[LF_MAX_FRAMES];
 };
 
@@ -621,7 +621,7 @@ __device__ __forceinline__ void bwd_tile(const BwdParams& P, const Dims& D, cons
       uint64_t* full = &bars[side0 ? kBbRing0 : kBbRing1];
       uint64_t* empty = full + n_slot;
       uint8_t* ring = smem + (side0 ? L::kR0 : L::kR1);
-      const bool stall = P.debug_stall && blockIdx.x == 0;
+      const bool stall = P.debug_stall == (int)blockIdx.x + 1;
       if (side0 && run && !stall) {
         expect_if(lead, &bars[kBbIn], 2 * L::kTile);
         if (!is_dq && kt.kind == 0) {

@@ -380,7 +380,10 @@ int lf_forward_chunk(const lf_shape* shape, const void* q, const void* k_cur,
  *   stall          nonzero: the first CTA of each attention launch never arms its query
  *                  barrier, so its waits run out after wait_limit_ns; the launch then
  *                  drains, frees its tensor memory, returns, and lf_device_status()
- *                  reports LF_ERR_TIMEOUT (that launch's output is undefined);
+ *                  reports LF_ERR_TIMEOUT (that launch's output is undefined).  In the
+ *                  gradient's launch it is CTA stall - 1, whose own tiles never come: the
+ *                  query tiles come first, then the key tiles (dense, sinks, with lists);
+ *                  a key tile that no query attends to does not wait;
  *   tail_split     zero: every query tile is computed whole (no split of the last partial
  *                  wave into key ranges), so each tile's rounding is independent of how
  *                  many tiles a launch has.

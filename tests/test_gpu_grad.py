@@ -357,3 +357,37 @@ def test_detached_dense_chunk_makes_no_block_boxes(gpu_lib):
     plans = 4 * sh.H * tiles * (1 + sh.n_sink * nb + 2 * kf * kb) + 4
     dense = sh.H * 2 * -(-sh.n_cur_frames * sh.T // 128) * 512
     assert int((ws != 255).sum()) <= plans + dense
+
+
+@pytest.mark.parametrize("kind", ["dense", "sink", "history", "current"])
+def test_stalled_key_tiles_time_out(gpu_lib, kind):
+    """The waits of the dk, dv pass made to run out: a key tile's own rows never arrive.  CTAs
+    are the query tiles, then the key tiles: dense current chunk, sinks, those with lists."""
+    ci = small(18, T=200, H=2, d=128, k_c=3 if kind == "current" else 0)
+    sh = ci.shape
+    t = G.to_dev(ci)
+    bidx, cidx = lists(sh, 0)
+    out, lse = forward(ci, t, bidx, cidx)
+    dout = dout_for(ci)
+    nb, nqb, _, _ = lf.derived(sh)
+    per_frame = -(-sh.T // 128)
+    dense = 0 if kind == "current" else -(-sh.n_cur_frames * sh.T // 128) * sh.H
+    first = -(-nqb // 2) * sh.H
+    lists_at = first + dense + sh.n_sink * per_frame * sh.H
+    if kind == "history":                                 # the first tile that a list names
+        block = int(bidx[0].min())
+        cta = lists_at + block // nb * per_frame + block % nb // 2
+    elif kind == "current":
+        block = int(cidx[0].min())
+        cta = lists_at + block // nb * per_frame + block % nb // 2
+    else:
+        cta = first + (dense if kind == "sink" else 0)
+    assert lf.lf_device_status(True) == 0
+    try:
+        lf.lf_debug_configure(wait_limit_ns=20_000_000, stall=cta + 1)
+        backward(ci, t, bidx, cidx, out, dout, lse)
+        torch.cuda.synchronize()
+    finally:
+        lf.lf_debug_configure()
+    assert lf.lf_device_status(True) == 4                 # LF_ERR_TIMEOUT
+    run_case(ci)
