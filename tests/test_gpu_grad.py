@@ -391,3 +391,128 @@ def test_stalled_key_tiles_time_out(gpu_lib, kind):
         lf.lf_debug_configure()
     assert lf.lf_device_status(True) == 4                 # LF_ERR_TIMEOUT
     run_case(ci)
+
+
+def test_dropped_history_beside_a_valid_current_list(gpu_lib, monkeypatch):
+    """A bad history id drops the history of its query tile (two blocks of 64) and nothing else:
+    the current-chunk lists stay, and the cache's gradient leaves those queries out."""
+    ci = small(19, T=100, H=2, d=128, n_hist=4, n_sink=1, k_f=2, k_b=2, k_c=2)
+    sh = ci.shape
+    t = G.to_dev(ci)
+    bidx, cidx = lists(sh, 5)
+    good = bidx.clone()
+    bidx[1, 2, -1] = 4 * 2                                # one past the last block: blocks 2, 3
+    out, lse = forward(ci, t, bidx, cidx)
+    assert lf.lf_device_status(True) == LF_ERR_BAD_INDEX
+    dout = dout_for(ci)
+    g = backward(ci, t, bidx, cidx, out, dout, lse)
+    assert lf.lf_device_status(True) == LF_ERR_BAD_INDEX
+    visible = R.visible
+
+    def without(shape, block_idx, cur_idx, h, device):
+        see = visible(shape, block_idx, cur_idx, h, device)
+        if h == 1:
+            see[100:, 200 + 100:] = False                 # frame 1: query blocks 2 and 3
+        return see
+
+    monkeypatch.setattr(R, "visible", without)
+    r = R.attention_backward(sh, t["q"], t["k_cur"], t["v_cur"], t["k_cache"], t["v_cache"],
+                             ci.hist_slots, ci.sink_slots, good, cidx, dout, out, lse)
+    listed = list(ci.sink_slots) + list(ci.hist_slots)
+    for n in ("dq", "dk_cur", "dv_cur"):
+        check(n, g[n], r[n])
+    for n in ("dk_cache", "dv_cache"):
+        check(n, g[n][listed], {w: x[listed] for w, x in r[n].items()})
+
+
+def test_cache_gradient_through_the_layer(gpu_lib):
+    """The cache's gradient under the lists that lf_forward_chunk chose, and its status."""
+    ci = small(20, T=300, H=3, d=128, n_cur_frames=2, n_hist=5, n_sink=1, k_f=3, k_b=2, k_c=4)
+    t = G.to_dev(ci)
+    out, lse, bidx, cidx = G.gpu_forward(ci, t, with_cur=True)
+    dout = dout_for(ci)
+    g = backward(ci, t, bidx, cidx, out, dout, lse)
+    torch.cuda.synchronize()
+    assert lf.lf_device_status(True) == 0
+    r = R.attention_backward(ci.shape, t["q"], t["k_cur"], t["v_cur"], t["k_cache"], t["v_cache"],
+                             ci.hist_slots, ci.sink_slots, bidx, cidx, dout, out, lse)
+    listed = list(ci.sink_slots) + list(ci.hist_slots)
+    for n in ("dk_cache", "dv_cache"):
+        check(n, g[n][listed], {w: x[listed] for w, x in r[n].items()})
+
+
+def _same_bits(a, b):
+    return (a.view(torch.int16) == b.view(torch.int16)).all(-1)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_reach_of_a_bad_gradient_row(gpu_lib, value):
+    """An infinity or NaN in one row of dout reaches that query's tile (two blocks of 64) in dq and
+    the key tiles (128 rows of a frame) that its block attends to, and nothing further: every
+    other gradient keeps its bits."""
+    ci = small(21, T=300, H=2, d=128, n_cur_frames=2, n_hist=6, n_sink=0, k_f=1, k_b=2, k_c=2)
+    sh = ci.shape
+    t = G.to_dev(ci)
+    bidx, cidx = lists(sh, 6)
+    out, lse = forward(ci, t, bidx, cidx)
+    dout = dout_for(ci)
+    want = backward(ci, t, bidx, cidx, out, dout, lse)
+    nb = lf.derived(sh)[0]
+    qb, row = nb + 1, sh.T + 64 + 10                      # second block of the second frame
+    dout[row, 1, 3] = value
+    got = backward(ci, t, bidx, cidx, out, dout, lse)
+    assert bool(got["dq"][row, 1].isnan().any())
+    frame, blk = torch.arange(2 * sh.T) // sh.T, torch.arange(2 * sh.T) % sh.T // 64
+    tile = (frame * nb + blk) // 2 == qb // 2
+    clean = torch.ones(2 * sh.T, sh.H, dtype=torch.bool)
+    clean[tile, 1] = False
+    assert bool(_same_bits(got["dq"], want["dq"]).cpu()[clean].all())
+
+    def check_keys(names, chosen, n_frames, rows):
+        """chosen: block ids of the row's list; rows: gradient rows in frame order."""
+        bad = torch.zeros(n_frames * sh.T, dtype=torch.bool)
+        for g in chosen:
+            f, b = g // nb, g % nb
+            bad[f * sh.T + b // 2 * 128:f * sh.T + min(sh.T, b // 2 * 128 + 128)] = True
+        assert not bool(bad.all())
+        for n in names:
+            x, y = rows(got[n]), rows(want[n])
+            assert bool(_same_bits(x, y).cpu()[~bad, 1].all()) and bool(_same_bits(x, y)[:, 0].all()), n
+            assert bool(x[:, 1].isfinite().logical_not().any()), n
+
+    check_keys(("dk_cur", "dv_cur"), cidx[1, qb].tolist(), 2, lambda x: x)
+    check_keys(("dk_cache", "dv_cache"), bidx[1, qb].tolist(), 6,
+               lambda x: x[list(ci.hist_slots)].reshape(-1, sh.H, sh.d))
+
+
+@pytest.mark.parametrize("name", ["k_cache", "v_cache"])
+def test_reach_of_a_bad_key_row(gpu_lib, name):
+    """A NaN in one cached key or value row reaches the query tiles whose plan holds its block and
+    the gradients of its own key tile, and nothing further (out and lse of the clean pass)."""
+    ci = small(22, T=300, H=2, d=128, n_cur_frames=2, n_hist=6, n_sink=0, k_f=1, k_b=2, k_c=2)
+    sh = ci.shape
+    t = G.to_dev(ci)
+    bidx, cidx = lists(sh, 7)
+    out, lse = forward(ci, t, bidx, cidx)
+    dout = dout_for(ci)
+    want = backward(ci, t, bidx, cidx, out, dout, lse)
+    nb, nqb, _, _ = lf.derived(sh)
+    bad = int(bidx[1, 4, 0])
+    slot, at = ci.hist_slots[bad // nb], bad % nb * 64 + 5
+    t[name][slot, at, 1, 2] = float("nan")
+    got = backward(ci, t, bidx, cidx, out, dout, lse)
+    holds = (bidx[1] == bad).any(-1).cpu()
+    tiles = {q // 2 for q in range(nqb) if holds[q]}
+    assert len(tiles) < -(-nqb // 2)
+    tok = torch.arange(2 * sh.T)
+    qb = tok // sh.T * nb + tok % sh.T // 64
+    clean = torch.ones(2 * sh.T, sh.H, dtype=torch.bool)
+    clean[torch.tensor([int(x) // 2 in tiles for x in qb]), 1] = False
+    assert bool(_same_bits(got["dq"], want["dq"]).cpu()[clean].all())
+    assert bool(got["dq"][:, 1].isnan().any())
+    for n in ("dk_cur", "dv_cur"):
+        assert bool(_same_bits(got[n], want[n]).all()), n
+    clean = torch.ones(sh.n_slots, sh.T, sh.H, dtype=torch.bool)
+    clean[slot, at // 128 * 128:at // 128 * 128 + 128, 1] = False
+    for n in ("dk_cache", "dv_cache"):
+        assert bool(_same_bits(got[n], want[n]).cpu()[clean].all()), n
