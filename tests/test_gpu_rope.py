@@ -247,3 +247,42 @@ def test_gradient_of_very_small_and_large_rows(gpu_lib, norm, power):
     c["x"].mul_(2.0 ** power)                              # exact
     c["dout"] = (check_forward(c).float() + 0.5 * c["dout"].float()).to(torch.bfloat16)
     check_backward(c, wide=True)
+
+
+# Sizes of the kernel that gives a thread four tokens of one unit each (2000 groups of threads and
+# more), with last groups that are not full: both warp layouts (a token in part of a warp, in
+# several warps), both head dimensions, both kernel-argument sizes.
+MANY = [
+    dict(H=12, d=128, frames=3, height=29, width=53),
+    dict(H=12, d=128, frames=3, height=29, width=53, slots=5, out_slots=7, strided=True),
+    dict(H=12, d=64, frames=5, height=41, width=43, slots=6),
+    dict(H=12, d=128, frames=40, height=7, width=15, slots=44, out_slots=45, strided=True),
+    dict(H=2, d=128, frames=20, height=40, width=41, out_slots=21),
+]
+
+
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("norm", [None, "head", "row"])
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_values_of_many_tokens(gpu_lib, i, norm, halves):
+    c = case(norm=norm, halves=halves, seed=40 + i, pos=[3 * f - 7 for f in range(MANY[i]["frames"])],
+             **MANY[i])
+    check_forward(c)
+    check_backward(c, wide=bool(i & 1))
+
+
+@pytest.mark.parametrize("norm", [None, "head", "row"])
+@pytest.mark.parametrize("H, d, frames, height, width", [(5, 64, 3, 4, 7), (40, 128, 3, 5, 9),
+                                                         (12, 128, 3, 30, 52)])
+def test_gradient_in_place(gpu_lib, norm, H, d, frames, height, width):
+    """dx may be dout, where strides and slots agree: the same bits, other slots untouched."""
+    c = case(H, d, frames, height, width, norm=norm, slots=5, out_slots=5, seed=50)
+    c["outs"] = c["ins"]
+    _, want, dw = backward(c)
+    same, dw2 = c["dout"].clone(), None if dw is None else torch.empty_like(dw)
+    lf.lf_rope_frames_backward(c["rope"], c["x"], same, same, weight=c["weight"], dweight=dw2,
+                               in_slots=c["ins"], out_slots=c["outs"])
+    assert torch.equal(same[c["ins"]], want[c["ins"]])
+    rest = [s for s in range(5) if s not in c["ins"]]
+    assert torch.equal(same[rest], c["dout"][rest])
+    assert dw is None or torch.equal(dw, dw2)
