@@ -639,6 +639,7 @@ int make_rope(const lf_rope* r, int32_t n_in, const int32_t* in_slots, const int
     const int n = p < A->p_t ? r->pairs_t : p < A->p_h ? r->pairs_h : r->pairs_w;
     const int i = p < A->p_t ? p : p < A->p_h ? p - A->p_t : p - A->p_h;
     A->turns[p] = std::pow(r->base, -(double)i / n) / 6.283185307179586477;
+    if (!std::isfinite(A->turns[p])) return LF_ERR_INVALID_ARG;
   }
   A->halves = r->halves;
   A->norm = r->norm;

@@ -258,7 +258,7 @@ typedef struct lf_rope {
     int32_t norm;             /* LF_NORM_*                                                 */
     float eps;                /* added to the mean square, >= 0                            */
     double base;              /* frequency base, > 0: pair i of an axis with n pairs turns by
-                                 position * base^(-i / n) radians                          */
+                                 position * base^(-i / n) radians (each finite)            */
 } lf_rope;
 
 /* out[frame, t, h] = R(position) (w * x * r), r = 1 / sqrt(mean(x^2) + eps) over the norm's

@@ -122,3 +122,11 @@ def test_32_bit_lists_pass_unchanged():
         pointer, keep = lf._slots(v)
         assert list(keep) == ends and pointer[3] == ends[3]
     assert len(lf._slots([])[1]) == 1
+
+
+def test_rope_frequencies_are_finite(lib):
+    """A base so small that base^(-i / n) overflows would turn by NaN, at position zero too."""
+    assert _rope(lib, base=5e-324, pairs=(32, 0, 0)) == 1
+    assert _rope(lib, base=5e-324, pairs=(0, 0, 32)) == 1
+    assert lf.lf_rope_backward_workspace_size(
+        lf.make_rope(2, 64, 3, 4, 5, (32, 0, 0), norm="row", base=5e-324)) == 0
