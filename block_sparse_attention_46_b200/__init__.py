@@ -34,6 +34,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblf.so")
 
 LF_OK = 0
 LF_ERR_INVALID_ARG = 1
+LF_ERR_UNSUPPORTED = 2
 
 
 class LfError(RuntimeError):
@@ -459,6 +460,8 @@ def lf_block_sparse_attn_backward(shape, q, k_cur, v_cur, k_cache, v_cache, hist
     dev, bf, i32 = _on_gpu(what, "q", q), torch.bfloat16, torch.int32
     if len(hist_slots) != sh.n_hist or len(sink_slots) != sh.n_sink:
         raise ValueError(f"{what}: slot lists do not match the shape's frames")
+    if sh.d < 1 or sh.block < 1:
+        _check(LF_ERR_UNSUPPORTED, what)
     _, nqb, kf, kb = derived(shape)
     row = sh.H * sh.d
     chunk = sh.n_cur_frames * sh.tokens_per_frame * row

@@ -516,3 +516,15 @@ def test_reach_of_a_bad_key_row(gpu_lib, name):
     clean[slot, at // 128 * 128:at // 128 * 128 + 128, 1] = False
     for n in ("dk_cache", "dv_cache"):
         assert bool(_same_bits(got[n], want[n]).cpu()[clean].all()), n
+
+
+@pytest.mark.parametrize("bad", [dict(d=0), dict(d=96), dict(block=0), dict(block=32), dict(H=0)])
+def test_unsupported_shapes_are_library_errors(gpu_lib, bad):
+    """Shapes that the library refuses are its errors (or the binding's, for tensors that do not
+    fit them), with d or block zero too."""
+    ci = small(15, T=100)
+    t = G.to_dev(ci)
+    bidx, cidx = lists(ci.shape, 0)
+    out, lse = forward(ci, t, bidx, cidx)
+    with pytest.raises(lf.LfError if 0 in (bad.get("d"), bad.get("block")) else ValueError):
+        backward(replace(ci, shape=replace(ci.shape, **bad)), t, bidx, cidx, out, dout_for(ci), lse)
