@@ -691,8 +691,9 @@ lf::RopeArgs<lf::kRopeFewFrames> few_frames(const RopeCall& A, int n) {
 template <int NF>
 int launch_rope_nf(const lf::RopeArgs<NF>& A, cudaStream_t st) {
   const int u = lf::cdiv(A.units, A.tpt);
-  const int nt = u == 1 && rope_smem(A, false, lf::kRopeTokens) <= 48 * 1024 &&
-                 (int64_t)A.n_frames * lf::cdiv(A.T, A.groups) >= lf::kRopeManyGroups
+  const int nt = u == 1 && A.tpt * A.groups >= lf::kRopeManyThreads &&
+                 (int64_t)A.n_frames * lf::cdiv(A.T, A.groups) >= lf::kRopeManyCtas &&
+                 rope_smem(A, false, lf::kRopeTokens) <= 48 * 1024
                      ? lf::kRopeTokens : 1;
   auto kern = nt > 1   ? lf::rope_kernel<1, lf::kRopeTokens, NF>
               : u == 1 ? lf::rope_kernel<1, 1, NF>

@@ -27,11 +27,17 @@ constexpr int kRopeMaxPairs = 64;            // d / 2
 constexpr int kRopeUnits = 3;                // 16-channel units per thread, at most
 constexpr int kRopeThreads = 256;            // per CTA, at most; a token's threads are in one CTA
 static_assert(kRopeUnits * 16 * kRopeThreads == LF_MAX_ROPE_CHANNELS, "the widest token");
-// Forward, wide tokens: tokens per thread where there are this many groups of threads for
-// them (24 cached frames: 43 us against 45 with one token each, the 480p queries 15.7
-// against 17.5); below, one, for the latency of small calls.
-constexpr int kRopeTokens = 4, kRopeManyGroups = 2000;
-constexpr int kRopeBwdCtas = 296;            // backward with a norm: CTAs (partial sums of dw), at most
+// Forward, tokens of one unit per thread: with four tokens per thread a long call has more loads
+// in flight, a shorter one fewer CTAs than it needs.  By the CTAs of one token per thread, four
+// tokens against one: from 2000 to 9000 up to 40 % slower (10 % faster in one case, where a wave
+// just fills), level between 9000 and 16000, from there 0.88 to 1.03 of the time, 0.97 for 24
+// cached frames.  CTAs of 160 threads (20 heads of 128, 40 of 64) do not gain at any size; one
+// head alone has too many tokens per CTA for four times their angles (64 KB).
+constexpr int kRopeTokens = 4, kRopeManyCtas = 16000, kRopeManyThreads = 192;
+// Backward with a norm: CTAs, each with a partial sum of dw, at most: the two that an SM's
+// registers hold, on 148 SMs.  A constant, so that dw's order of additions, and with it its bits,
+// and the workspace do not depend on the device.
+constexpr int kRopeBwdCtas = 296;
 
 struct RopeHead {
   const __nv_bfloat16* x;      // rows of H * d channels, x_stride elements apart

@@ -249,15 +249,16 @@ def test_gradient_of_very_small_and_large_rows(gpu_lib, norm, power):
     check_backward(c, wide=True)
 
 
-# Sizes of the kernel that gives a thread four tokens of one unit each (2000 groups of threads and
-# more), with last groups that are not full: both warp layouts (a token in part of a warp, in
-# several warps), both head dimensions, both kernel-argument sizes.
+# Calls of several waves, with last groups that are not full, up to those whose threads take four
+# tokens each (16000 CTAs of one token per thread and more): both warp layouts (a token in part
+# of a warp, in several warps), both head dimensions, few and many frames.
 MANY = [
     dict(H=12, d=128, frames=3, height=29, width=53),
-    dict(H=12, d=128, frames=3, height=29, width=53, slots=5, out_slots=7, strided=True),
     dict(H=12, d=64, frames=5, height=41, width=43, slots=6),
-    dict(H=12, d=128, frames=40, height=7, width=15, slots=44, out_slots=45, strided=True),
-    dict(H=2, d=128, frames=20, height=40, width=41, out_slots=21),
+    dict(H=12, d=128, frames=3, height=101, width=107, slots=5, out_slots=7, strided=True),
+    dict(H=9, d=64, frames=3, height=101, width=217, slots=4),
+    dict(H=12, d=128, frames=40, height=7, width=117, slots=44, out_slots=45, strided=True),
+    dict(H=2, d=128, frames=20, height=113, width=115, out_slots=21),
 ]
 
 
