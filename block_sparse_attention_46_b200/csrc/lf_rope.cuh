@@ -29,8 +29,8 @@ constexpr int kRopeThreads = 256;            // per CTA, at most; a token's thre
 static_assert(kRopeUnits * 16 * kRopeThreads == LF_MAX_ROPE_CHANNELS, "the widest token");
 // Forward, tokens of one unit per thread: with four tokens per thread a long call has more loads
 // in flight, a shorter one fewer CTAs than it needs.  By the CTAs of one token per thread, four
-// tokens against one: from 2000 to 9000 up to 40 % slower (10 % faster in one case, where a wave
-// just fills), level between 9000 and 16000, from there 0.88 to 1.03 of the time, 0.97 for 24
+// tokens against one: from 2000 to 9000 up to 40 % slower (at best 8 % faster, where a wave just
+// fills), 0.95 to 1.03 of the time between 9000 and 16000, from there 0.88 to 1.01, 0.97 for 24
 // cached frames.  CTAs of 160 threads (20 heads of 128, 40 of 64) do not gain at any size; one
 // head alone has too many tokens per CTA for four times their angles (64 KB).
 constexpr int kRopeTokens = 4, kRopeManyCtas = 16000, kRopeManyThreads = 192;

@@ -528,3 +528,46 @@ def test_unsupported_shapes_are_library_errors(gpu_lib, bad):
     out, lse = forward(ci, t, bidx, cidx)
     with pytest.raises(lf.LfError if 0 in (bad.get("d"), bad.get("block")) else ValueError):
         backward(replace(ci, shape=replace(ci.shape, **bad)), t, bidx, cidx, out, dout_for(ci), lse)
+
+
+def test_slots_past_32_bits(gpu_lib):
+    """Frames in slots whose elements lie past 2^31 (and 2^32 bytes) give the bits of the same
+    frames in the first slots: rotation into and out of them, the attention, its gradient."""
+    T, H, d, grid = 1560, 12, 128, (30, 52)
+    far, n_far = [899, 897, 898], 900
+    assert far[1] * T * H * d > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    old, cur, grad = rand(3, T, 3, H, d), rand(T, 3, H, d), rand(T, H, d)
+    weight = 1 + 0.1 * torch.randn(H * d, generator=g, device="cuda")
+    rope = lf.make_rope(H, d, 3, *grid, (24, 20, 20), norm="row")
+    bidx = None
+
+    def run(slots, n_slots):
+        nonlocal bidx
+        k_cache, v_cache, dkc, dvc = (torch.zeros(n_slots, T, H, d, dtype=torch.bfloat16, device="cuda")
+                                      for _ in range(4))
+        lf.lf_rope_frames(rope, old[:, :, 1], k_cache, weight=weight, out_slots=slots)
+        v_cache[slots] = old[:, :, 2]
+        sh = W.Shape(H=H, d=d, T=T, block=64, n_cur_frames=1, n_hist=2, n_sink=1, n_slots=n_slots,
+                     k_f=2, k_b=5, scale=d ** -0.5)
+        if bidx is None:
+            bidx = lists(sh, 3)[0]
+        q, k, v = (cur[:, i].contiguous() for i in range(3))
+        out, lse = torch.empty_like(q), torch.empty(H, T, device="cuda")
+        lf.lf_block_sparse_attn(sh, q, k, v, k_cache, v_cache, slots[:2], slots[2:], bidx, out, lse)
+        res = [torch.empty_like(q) for _ in range(3)]
+        lf.lf_block_sparse_attn_backward(sh, q, k, v, k_cache, v_cache, slots[:2], slots[2:], bidx,
+                                         out, grad, lse, *res, dkc, dvc)
+        dx, dw = torch.zeros_like(old)[:, :, 1], torch.empty_like(weight)
+        lf.lf_rope_frames_backward(rope, old[:, :, 1], dkc, dx, weight=weight, dweight=dw,
+                                   out_slots=slots)
+        moved = torch.empty(3, T, H, d, dtype=torch.bfloat16, device="cuda")
+        lf.lf_rope_frames(lf.make_rope(H, d, 3, *grid, (24, 20, 20)), k_cache, moved, in_slots=slots)
+        return [out, lse, *res, k_cache[slots], dkc[slots], dvc[slots], dx, dw, moved]
+
+    near = run([0, 1, 2], 3)
+    for i, (a, b) in enumerate(zip(near, run(far, n_far))):
+        assert torch.equal(a, b), i
+    assert lf.lf_device_status(True) == 0
+    assert all(bool(x.isfinite().all()) and bool((x != 0).any()) for x in near)
