@@ -8,6 +8,7 @@ does not load, every call raises.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import operator
@@ -160,13 +161,16 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _slots(v: Sequence[int]):
-    """Host list of int32 for a call.  ctypes would wrap what does not fit and int() cut off a
-    fraction, both silently."""
-    n = [int(x) for x in v]
-    if n and not (-2 ** 31 <= min(n) and max(n) < 2 ** 31 and all(map(operator.eq, n, v))):
-        raise ValueError(f"slots and positions are 32-bit integers, not {list(v)}")
+    """Host list of int32 for a call, and the memory to keep alive during it.  ctypes alone would
+    wrap what does not fit, silently."""
+    try:
+        n = array.array("i", v)                  # refuses what is no 32-bit integer
+    except (TypeError, OverflowError):
+        n = [int(x) for x in v]                  # 3.0 is one, 2.5 and 2^31 are not
+        if not (-2 ** 31 <= min(n) and max(n) < 2 ** 31 and all(map(operator.eq, n, v))):
+            raise ValueError(f"slots and positions are 32-bit integers, not {list(v)}") from None
     arr = (ctypes.c_int32 * max(len(n), 1))(*n)
-    return ctypes.cast(arr, _I32P), arr          # keep `arr` alive during the call
+    return arr, arr
 
 
 def _stream(stream) -> ctypes.c_void_p:
