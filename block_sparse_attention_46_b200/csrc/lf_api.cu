@@ -470,7 +470,9 @@ struct BwdWs {
   size_t bytes;
 };
 
-// forward attention workspace (key plans, partial dq of split tiles) | rows | transposed plans
+// forward attention workspace | rows | transposed plans.  Of the first only the key plans are
+// used (the gradient splits no tile, so its partial results stay idle); taken whole, a workspace
+// of the gradient is also one of lf_block_sparse_attn for the same shape.
 BwdWs carve_bwd(const Dims& D, void* base, int n_sm) {
   BwdWs w{};
   w.attn = carve_attn(D, base, n_sm);

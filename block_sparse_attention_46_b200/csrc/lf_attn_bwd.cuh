@@ -281,9 +281,13 @@ bwd_transpose_kernel(const uint32_t* __restrict__ plan, const int32_t* __restric
 // of the exponentials on the multiply-add units 1 %; own tiles loaded before the allocation
 // of tensor memory 2-3 %; no register split 3 %.
 //
-// P and dS enter their products rounded to bf16, as tensor-core operands have to be: each
-// product's term is off by 2^-8 relative at most.  Outputs' relative error is then 0.0024 to
-// 0.0025 against 64 bits; fp32 operands and one rounding at the end give 0.0017.
+// P and dS enter their products rounded to bf16, the type of the tensor-core operands beside
+// them (K, Q and dout): each term of a sum is off by at most 2^-8 of it, half a step.  Nothing
+// else is lost: fp32 with these two roundings and the final one gives the kernel's outputs to
+// within 3e-4, in one of 24 cases 1e-3.  Against 64 bits the outputs' relative error is 0.0022 to
+// 0.0025 where sums have dozens of terms or more and 0.0019 to 0.0033 where they have a few (one
+// to ten keys per row); with fp32 operands it is 0.0016 to 0.0018.  dq loses most, since
+// sum_k dS = 0 cancels what a row's keys have in common but not its rounding errors.
 //
 // A barrier that is waited for every other tile, or whose next completion does not depend on
 // the waiting thread, exists twice, one for even and one for odd tiles: a wait on a parity
@@ -335,7 +339,7 @@ struct BwdLayout {
   static constexpr int NH = HD / 64;
   static constexpr int kRegion = 128 * 128;            // 128 rows x 64 channels
   static constexpr int kTile = NH * kRegion;
-  static constexpr int kMisc = kBbCount * 8;           // tensor-memory address, abort flag
+  static constexpr int kMisc = kBbCount * 8;           // tensor-memory address
   static constexpr int kCols = 1024;                   // two tiles' boxes of row values
   static constexpr int kIn0 = kCols + 2 * 2 * kBoxFloats * 4;
   static constexpr int kIn1 = kIn0 + kTile;

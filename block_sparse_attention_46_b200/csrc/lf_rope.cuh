@@ -7,8 +7,10 @@
 // Gradient: g = R(-theta) dy; dw = sum over tokens of g * xn (and over heads for the
 // per-head weight); dx = r * (w g - xn * mean(w g xn)), the mean over the norm's channels.
 //
-// Large calls are bound by memory: 4 bytes per element forward, 6 backward with a norm (24 cached
-// frames: 43-45 us, 0.78-0.82 of the copy rate); small ones by the host's side of the call.  A token
+// 4 bytes per element forward, 6 backward with a norm.  Large calls without a norm are bound by
+// memory (24 frames of 1560 x 12 x 128: 43-45 us, 0.78-0.82 of the copy rate, gradient 42 us); with
+// one, warps wait for sums and weights (into cache slots 60 us, 0.58 of the copy rate, norm per
+// head 54; gradient 133 us, 0.40, per head 111).  Small calls: the host's side of the call.  A token
 // is held in the registers of `tpt` threads (4 to 32 lanes of a warp, or several warps for
 // wide tokens), 16 channels (two 16-byte loads) per unit and up to kRopeUnits units per
 // thread, so x is read once although the norm needs a sum over it first.  A unit is 8 channels

@@ -223,12 +223,16 @@ int lf_block_sparse_attn(const lf_shape* shape, const void* q, const void* k_cur
  * left as they were, and a slot listed twice is LF_ERR_INVALID_ARG (its two gradients would
  * meet in one place).  Outputs must not overlap inputs or each other.  A row that attends to
  * nothing (lse = -inf) gets dq = 0 and gives nothing to dk and dv.  Products run on bf16
- * tensor cores with P and dS rounded to bf16, sums in fp32; each gradient is rounded once.
+ * tensor cores with P and dS rounded to bf16 (2^-8 of a term at most, so about 1.5 times the
+ * error of the final rounding alone, twice where a sum has only a few terms), sums in fp32;
+ * each gradient is rounded once.
  * As in the forward pass, tiles are 128 rows: an infinity or NaN in a row may also reach the
  * gradients of rows that attend to its tile, or share it, without attending to that row.
  * workspace: at least lf_attn_backward_workspace_size(shape) bytes, 256-byte aligned, for
  * this call alone until it has finished on the GPU.  LF_ERR_BAD_INDEX and LF_ERR_TIMEOUT as
- * for lf_block_sparse_attn, but the waits' limit (2 s) counts from the start of each CTA. */
+ * for lf_block_sparse_attn, but the waits of a CTA have one limit together, 4e9 SM clocks from
+ * its start (2 s at 2 GHz, longer at lower clocks), and what is then still in flight has as
+ * long again. */
 size_t lf_attn_backward_workspace_size(const lf_shape* shape);
 int lf_block_sparse_attn_backward(const lf_shape* shape, const void* q, const void* k_cur,
                                   const void* v_cur, const void* k_cache, const void* v_cache,
@@ -376,7 +380,7 @@ int lf_forward_chunk(const lf_shape* shape, const void* q, const void* k_cur,
 /* Test hook, not part of the attention path (process-wide, not thread-safe; call it only
  * while no library work is queued).  Sets, for the attention launches that follow:
  *   wait_limit_ns  the limit of every bounded device wait (0 = the default, 2 s; at most
- *                  20 s);
+ *                  20 s); in the gradient 2 SM clocks per ns, from each CTA's start;
  *   stall          nonzero: the first CTA of each attention launch never arms its query
  *                  barrier, so its waits run out after wait_limit_ns; the launch then
  *                  drains, frees its tensor memory, returns, and lf_device_status()
